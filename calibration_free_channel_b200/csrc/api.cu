@@ -236,6 +236,38 @@ moe_status run_forward(const moe_reader_layer* L, int B, int k, int c, const uin
   return MOE_OK;
 }
 
+// The grouped entry points.
+constexpr size_t kErrBytes = 256;          // the device error word's slot at the head of a workspace
+constexpr int kMaxBlockTokens = 32768;     // moe_reader_forward_grouped
+
+#define REQUIRE_WIDTH(n)                                                                             \
+  REQUIRE((n) >= 8 && (n) <= moe::kMaxWidth && (n) % 8 == 0, "%s = %d is not a multiple of 8 in [8, %d]", #n, \
+          (int)(n), moe::kMaxWidth)
+
+moe_status check_plan(int n_groups, int n_rows, const char* rows_name) {
+  REQUIRE(n_groups >= 1 && n_groups <= moe::kMaxGroups, "%d groups: outside [1, %d]", n_groups, moe::kMaxGroups);
+  REQUIRE(n_rows >= 1 && n_rows <= moe::kMaxRows, "%s = %d outside [1, %d]", rows_name, n_rows, moe::kMaxRows);
+  return MOE_OK;
+}
+
+moe_status check_gather(int n_rows, int n_x, const uint16_t* x, const int32_t* x_rows, int x_div) {
+  REQUIRE_PTR(x);
+  OPT_PTR(x_rows);
+  REQUIRE(n_x >= 1 && n_x <= moe::kMaxRows, "n_x = %d outside [1, %d]", n_x, moe::kMaxRows);
+  REQUIRE(x_div >= 1, "x_div = %d must be >= 1", x_div);
+  if (!x_rows) {
+    REQUIRE(x_div == 1, "x_div = %d without x_rows", x_div);
+    REQUIRE(n_x >= n_rows, "n_x = %d < n_rows = %d without x_rows", n_x, n_rows);
+  }
+  return MOE_OK;
+}
+
+moe_status check_workspace(const void* workspace, size_t ws_bytes, size_t need) {
+  REQUIRE_PTR(workspace);
+  REQUIRE(ws_bytes >= need, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  return MOE_OK;
+}
+
 }  // namespace
 
 moe_status moe::set_last_error(moe_status st, const char* msg) {
@@ -376,6 +408,183 @@ moe_status moe_reader_forward_host(const moe_reader_layer* layer, int B, int k, 
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "device-to-host copy");
 }
 
+// ------------------------------------------- products over ragged groups
+size_t moe_reader_group_workspace_bytes(int n, int n_groups) {
+  if (n < 1 || n > moe::kMaxRows || n_groups < 1 || n_groups > moe::kMaxGroups) return 0;
+  return kErrBytes;
+}
+
+moe_status moe_reader_group_rows(int n, int n_groups, const int32_t* ids, int32_t* offsets, int32_t* rows,
+                                 void* workspace, size_t ws_bytes, void* stream) {
+  moe_status st = check_plan(n_groups, n, "n");
+  if (st != MOE_OK) return st;
+  REQUIRE_PTR(ids);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(rows);
+  st = check_workspace(workspace, ws_bytes, moe_reader_group_workspace_bytes(n, n_groups));
+  if (st != MOE_OK) return st;
+  cudaError_t e = moe::launch_group_rows(n, n_groups, ids, offsets, rows, static_cast<uint32_t*>(workspace),
+                                         static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "group_rows launch");
+}
+
+size_t moe_reader_grouped_workspace_bytes(int n_groups, int n_rows) {
+  if (n_rows < 1 || n_rows > moe::kMaxRows || n_groups < 1 || n_groups > moe::kMaxGroups) return 0;
+  return kErrBytes;
+}
+
+moe_status moe_reader_grouped_swiglu(int n_groups, int n_rows, int n_x, int I, int d, const uint16_t* x,
+                                     const int32_t* x_rows, int x_div, const int32_t* offsets,
+                                     const uint16_t* w_gate, const uint16_t* w_up, uint16_t* a, void* workspace,
+                                     size_t ws_bytes, void* stream) {
+  moe_status st = check_plan(n_groups, n_rows, "n_rows");
+  if (st != MOE_OK) return st;
+  st = check_gather(n_rows, n_x, x, x_rows, x_div);
+  if (st != MOE_OK) return st;
+  REQUIRE(I >= 1 && I <= moe::kMaxWidth, "I = %d outside [1, %d]", I, moe::kMaxWidth);
+  REQUIRE_WIDTH(d);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(w_gate);
+  REQUIRE_PTR(w_up);
+  REQUIRE_PTR(a);
+  st = check_workspace(workspace, ws_bytes, moe_reader_grouped_workspace_bytes(n_groups, n_rows));
+  if (st != MOE_OK) return st;
+  moe::GroupedArgs g = {};
+  g.G = n_groups;
+  g.P = n_rows;
+  g.n_x = n_x;
+  g.n_y = n_rows;
+  g.N = I;
+  g.K = d;
+  g.x = x;
+  g.x_rows = x_rows;
+  g.x_div = x_div;
+  g.offsets = offsets;
+  g.w = w_gate;
+  g.w_up = w_up;
+  g.y = a;
+  g.err = static_cast<uint32_t*>(workspace);
+  cudaError_t e = moe::launch_grouped(g, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "grouped_swiglu launch");
+}
+
+moe_status moe_reader_grouped_product(int n_groups, int n_rows, int n_x, int n_y, int N, int K, int w_layout,
+                                      const uint16_t* x, const int32_t* x_rows, int x_div, const int32_t* offsets,
+                                      const uint16_t* w, uint16_t* y, const int32_t* y_rows, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  moe_status st = check_plan(n_groups, n_rows, "n_rows");
+  if (st != MOE_OK) return st;
+  st = check_gather(n_rows, n_x, x, x_rows, x_div);
+  if (st != MOE_OK) return st;
+  REQUIRE_WIDTH(N);
+  REQUIRE_WIDTH(K);
+  REQUIRE(w_layout == 0 || w_layout == 1, "w_layout = %d: use 0 ([n_groups, N, K]) or 1 ([n_groups, K, N])", w_layout);
+  REQUIRE(n_y >= 1 && n_y <= moe::kMaxRows, "n_y = %d outside [1, %d]", n_y, moe::kMaxRows);
+  REQUIRE(y_rows || n_y >= n_rows, "n_y = %d < n_rows = %d without y_rows", n_y, n_rows);
+  OPT_PTR(y_rows);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(w);
+  REQUIRE_PTR(y);
+  st = check_workspace(workspace, ws_bytes, moe_reader_grouped_workspace_bytes(n_groups, n_rows));
+  if (st != MOE_OK) return st;
+  moe::GroupedArgs g = {};
+  g.G = n_groups;
+  g.P = n_rows;
+  g.n_x = n_x;
+  g.n_y = n_y;
+  g.N = N;
+  g.K = K;
+  g.layout = w_layout;
+  g.x = x;
+  g.x_rows = x_rows;
+  g.x_div = x_div;
+  g.offsets = offsets;
+  g.w = w;
+  g.y = y;
+  g.y_rows = y_rows;
+  g.err = static_cast<uint32_t*>(workspace);
+  cudaError_t e = moe::launch_grouped(g, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "grouped_product launch");
+}
+
+size_t moe_reader_adapter_workspace_bytes(int T, int n_adapters, int K, int N, int r) {
+  if (T < 1 || T > moe::kMaxRows || n_adapters < 1 || n_adapters > moe::kMaxGroups || K < 8 || N < 8 || r < 8 ||
+      r > 128)
+    return 0;
+  return kErrBytes;
+}
+
+moe_status moe_reader_adapter_product(int T, int n_adapters, int N, int K, int r, const uint16_t* x,
+                                      const uint16_t* w, const uint16_t* base, const int32_t* offsets,
+                                      const int32_t* rows, const uint16_t* a, const uint16_t* b,
+                                      const float* scale, uint16_t* y, void* workspace, size_t ws_bytes,
+                                      void* stream) {
+  moe_status st = check_plan(n_adapters, T, "T");
+  if (st != MOE_OK) return st;
+  REQUIRE_WIDTH(N);
+  REQUIRE_WIDTH(K);
+  REQUIRE(r >= 8 && r <= 128 && r % 8 == 0, "r = %d: need r in {8, 16, ..., 128}", r);
+  REQUIRE_PTR(x);
+  OPT_PTR(w);
+  OPT_PTR(base);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(rows);
+  REQUIRE_PTR(a);
+  REQUIRE_PTR(b);
+  OPT_PTR(scale);
+  REQUIRE_PTR(y);
+  REQUIRE(x != y, "y must not be x");
+  st = check_workspace(workspace, ws_bytes, moe_reader_adapter_workspace_bytes(T, n_adapters, K, N, r));
+  if (st != MOE_OK) return st;
+  const moe::AdapterArgs g = {T, n_adapters, N, K, r, x, w, base, offsets, rows, a, b, scale, y,
+                              static_cast<uint32_t*>(workspace)};
+  cudaError_t e = moe::launch_adapter(g, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "adapter_product launch");
+}
+
+size_t moe_reader_block_workspace_bytes(int B, int E, int top_e, int I, int d) {
+  if (B < 1 || B > kMaxBlockTokens || E < 1 || E > 1024 || top_e < 1 || top_e > 16 || I < 1 || d < 1) return 0;
+  return moe::block_layout(B, E, top_e, I, d, nullptr, nullptr);
+}
+
+moe_status moe_reader_forward_grouped(const moe_reader_layer* layer, int B, const uint16_t* x,
+                                      const uint16_t* residual, uint16_t* y, int32_t* ids, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  moe_status st = check_layer(layer, false);
+  if (st != MOE_OK) return st;
+  REQUIRE(B >= 1 && B <= kMaxBlockTokens, "B = %d outside [1, %d]", B, kMaxBlockTokens);
+  st = check_shape(1, layer->E, layer->top_e, layer->I, layer->d);
+  if (st != MOE_OK) return st;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(y);
+  REQUIRE(x != y, "y must not be x");
+  OPT_PTR(residual);
+  OPT_PTR(ids);
+  if (layer->expert_slot)
+    return fail(MOE_EUNSUPPORTED, "expert_slot (held experts only) is read by the streamed reader (path 0 or 2)");
+  st = check_workspace(workspace, ws_bytes,
+                       moe_reader_block_workspace_bytes(B, layer->E, layer->top_e, layer->I, layer->d));
+  if (st != MOE_OK) return st;
+  moe::BlockArgs g = {};
+  g.B = B;
+  g.E = layer->E;
+  g.I = layer->I;
+  g.d = layer->d;
+  g.top_e = layer->top_e;
+  g.x = x;
+  g.w_router = layer->w_router;
+  g.bias = layer->router_bias;
+  g.w_gate = layer->w_gate;
+  g.w_up = layer->w_up;
+  g.w_down = layer->w_down;
+  g.residual = residual;
+  g.y = y;
+  g.ids_out = ids;
+  moe::block_layout(B, layer->E, layer->top_e, layer->I, layer->d, workspace, &g);
+  cudaError_t e = moe::launch_block(g, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "grouped block launch");
+}
+
 moe_status moe_reader_rmsnorm(int B, int d, float eps, const uint16_t* x, uint16_t* h, void* stream) {
   REQUIRE(B >= 1 && B <= 65535, "B = %d outside [1, 65535]", B);
   REQUIRE(d >= 1 && d % 8 == 0, "d = %d must be a positive multiple of 8", d);
@@ -407,7 +616,7 @@ moe_status moe_reader_check_error(void* workspace, void* stream) {
   cudaMemcpy(ws.err, &zero, sizeof zero, cudaMemcpyHostToDevice);
   return fail((word & moe::kErrCopyTimeout) ? MOE_ETIMEOUT : MOE_EDEVICE,
               "device error word 0x%x (1: a bounded copy wait ran out; 2: bad work item; 4: a routed expert has no "
-              "weight slot)",
+              "weight slot; 8: a group plan is out of range)",
               word);
 }
 

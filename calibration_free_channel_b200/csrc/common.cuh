@@ -19,6 +19,7 @@ constexpr int kMaxTokens = 256;        // tokens per step (B)
 constexpr uint32_t kErrCopyTimeout = 1u;
 constexpr uint32_t kErrBadWorkItem = 2u;
 constexpr uint32_t kErrNoWeights = 4u;     // an active expert has no weight slot (expert_slot[e] < 0)
+constexpr uint32_t kErrBadPlan = 8u;       // a group plan's offset or row index is out of range
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
 
 // ------------------------------------------------------------------ bf16

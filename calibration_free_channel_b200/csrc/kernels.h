@@ -150,4 +150,67 @@ cudaError_t launch_rmsnorm(int B, int d, float eps, const uint16_t* x, uint16_t*
 // previous kernel by programmatic dependent launch.
 cudaError_t launch_copy16(const void* src, void* dst, size_t bytes, cudaStream_t s);
 
+// ---- products over ragged groups (grouped.cu, group_rows.cu, block.cu)
+constexpr int kMaxGroups = 1024;
+constexpr int kMaxRows = 1 << 20;
+constexpr int kMaxWidth = 32768;
+
+cudaError_t launch_group_rows(int n, int n_groups, const int32_t* ids, int32_t* offsets, int32_t* rows,
+                              uint32_t* err, cudaStream_t s);
+
+struct GroupedArgs {
+  int G, P, n_x, n_y, N, K;
+  int layout;               // 0: w [G, N, K]; 1: w [G, K, N]
+  const uint16_t* x;        // [n_x, K]
+  const int32_t* x_rows;    // [P] or null
+  int x_div;
+  const int32_t* offsets;   // [G + 1]
+  const uint16_t* w;        // the one matrix, or w_gate
+  const uint16_t* w_up;     // null: a plain product
+  void* y;                  // [n_y, N] bf16, or fp32 with y_fp32
+  int y_fp32;
+  const int32_t* y_rows;    // [P] or null
+  uint32_t* err;
+};
+cudaError_t launch_grouped(const GroupedArgs& a, cudaStream_t s);
+
+struct AdapterArgs {
+  int T, A, N, K, r;
+  const uint16_t* x;
+  const uint16_t* w;
+  const uint16_t* base;
+  const int32_t* offsets;
+  const int32_t* rows;
+  const uint16_t* a;
+  const uint16_t* b;
+  const float* scale;
+  uint16_t* y;
+  uint32_t* err;
+};
+cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s);
+
+struct BlockArgs {
+  int B, E, I, d, top_e;
+  const uint16_t* x;
+  const uint16_t* w_router;
+  const float* bias;
+  const uint16_t* w_gate;
+  const uint16_t* w_up;
+  const uint16_t* w_down;
+  const uint16_t* residual;
+  uint16_t* y;
+  int32_t* ids_out;   // or null
+  // workspace
+  uint32_t* err;
+  double* logits;     // [B, E]
+  int32_t* ids;       // [B, top_e]
+  float* wts;         // [B, top_e]
+  int32_t* offsets;   // [E + 1]
+  int32_t* rows;      // [B * top_e]
+  uint16_t* a;        // [B * top_e, I]
+  float* out;         // [B * top_e, d]
+};
+size_t block_layout(int B, int E, int top_e, int I, int d, void* base, BlockArgs* a);
+cudaError_t launch_block(const BlockArgs& a, cudaStream_t s);
+
 }  // namespace moe

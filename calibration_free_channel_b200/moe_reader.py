@@ -22,7 +22,15 @@ EXPORTS = ["moe_reader_workspace_bytes", "moe_reader_build_sketch", "moe_reader_
            "moe_reader_build_lowrank", "moe_reader_forward", "moe_reader_forward_dense",
            "moe_reader_forward_host", "moe_reader_rmsnorm", "moe_reader_check_error", "moe_reader_launch_plan",
            "moe_reader_forward_noalloc", "moe_reader_forward_ep", "moe_reader_ep_finish", "moe_reader_last_error",
-           "moe_reader_sketch_row_bytes", "moe_reader_sketch_to_base3"]
+           "moe_reader_sketch_row_bytes", "moe_reader_sketch_to_base3", "moe_reader_group_workspace_bytes",
+           "moe_reader_group_rows", "moe_reader_grouped_workspace_bytes", "moe_reader_grouped_swiglu",
+           "moe_reader_grouped_product", "moe_reader_adapter_workspace_bytes", "moe_reader_adapter_product",
+           "moe_reader_block_workspace_bytes", "moe_reader_forward_grouped"]
+
+# size queries return a byte count, moe_reader_last_error a string; every other function a status
+_NO_STATUS = {"moe_reader_workspace_bytes", "moe_reader_lowrank_workspace_bytes", "moe_reader_last_error",
+              "moe_reader_sketch_row_bytes", "moe_reader_group_workspace_bytes", "moe_reader_grouped_workspace_bytes",
+              "moe_reader_adapter_workspace_bytes", "moe_reader_block_workspace_bytes"}
 
 
 class MoeReaderLayer(C.Structure):
@@ -80,9 +88,21 @@ def lib():
         L.moe_reader_sketch_row_bytes.restype = sz
         L.moe_reader_sketch_row_bytes.argtypes = [i32, i32]
         L.moe_reader_sketch_to_base3.argtypes = [i32, i32, i32, P, P, P]
+        L.moe_reader_group_workspace_bytes.restype = sz
+        L.moe_reader_group_workspace_bytes.argtypes = [i32] * 2
+        L.moe_reader_group_rows.argtypes = [i32, i32, P, P, P, P, sz, P]
+        L.moe_reader_grouped_workspace_bytes.restype = sz
+        L.moe_reader_grouped_workspace_bytes.argtypes = [i32] * 2
+        L.moe_reader_grouped_swiglu.argtypes = [i32] * 5 + [P, P, i32, P, P, P, P, P, sz, P]
+        L.moe_reader_grouped_product.argtypes = [i32] * 7 + [P, P, i32, P, P, P, P, P, sz, P]
+        L.moe_reader_adapter_workspace_bytes.restype = sz
+        L.moe_reader_adapter_workspace_bytes.argtypes = [i32] * 5
+        L.moe_reader_adapter_product.argtypes = [i32] * 5 + [P] * 10 + [sz, P]
+        L.moe_reader_block_workspace_bytes.restype = sz
+        L.moe_reader_block_workspace_bytes.argtypes = [i32] * 5
+        L.moe_reader_forward_grouped.argtypes = [C.POINTER(MoeReaderLayer), i32, P, P, P, P, P, sz, P]
         for f in EXPORTS:
-            if f not in ("moe_reader_workspace_bytes", "moe_reader_lowrank_workspace_bytes", "moe_reader_last_error",
-                         "moe_reader_sketch_row_bytes"):
+            if f not in _NO_STATUS:
                 getattr(L, f).restype = C.c_int
         _lib = L
     return _lib
@@ -171,6 +191,53 @@ def moe_reader_forward_host(layer: MoeReaderLayer, B, k, c, x_host, x_dev, y_dev
                                          _ptr(y_host), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
+def moe_reader_group_workspace_bytes(n, n_groups) -> int:
+    return int(lib().moe_reader_group_workspace_bytes(n, n_groups))
+
+
+def moe_reader_group_rows(n, n_groups, ids, offsets, rows, workspace, ws_bytes, stream=None):
+    _check(lib().moe_reader_group_rows(n, n_groups, _ptr(ids), _ptr(offsets), _ptr(rows), _ptr(workspace), ws_bytes,
+                                       _stream(stream)))
+
+
+def moe_reader_grouped_workspace_bytes(n_groups, n_rows) -> int:
+    return int(lib().moe_reader_grouped_workspace_bytes(n_groups, n_rows))
+
+
+def moe_reader_grouped_swiglu(n_groups, n_rows, n_x, I, d, x, x_rows, x_div, offsets, w_gate, w_up, a, workspace,
+                              ws_bytes, stream=None):
+    _check(lib().moe_reader_grouped_swiglu(n_groups, n_rows, n_x, I, d, _ptr(x), _ptr(x_rows), x_div, _ptr(offsets),
+                                           _ptr(w_gate), _ptr(w_up), _ptr(a), _ptr(workspace), ws_bytes,
+                                           _stream(stream)))
+
+
+def moe_reader_grouped_product(n_groups, n_rows, n_x, n_y, N, K, w_layout, x, x_rows, x_div, offsets, w, y, y_rows,
+                               workspace, ws_bytes, stream=None):
+    _check(lib().moe_reader_grouped_product(n_groups, n_rows, n_x, n_y, N, K, w_layout, _ptr(x), _ptr(x_rows), x_div,
+                                            _ptr(offsets), _ptr(w), _ptr(y), _ptr(y_rows), _ptr(workspace), ws_bytes,
+                                            _stream(stream)))
+
+
+def moe_reader_adapter_workspace_bytes(T, n_adapters, K, N, r) -> int:
+    return int(lib().moe_reader_adapter_workspace_bytes(T, n_adapters, K, N, r))
+
+
+def moe_reader_adapter_product(T, n_adapters, N, K, r, x, w, base, offsets, rows, a, b, scale, y, workspace, ws_bytes,
+                               stream=None):
+    _check(lib().moe_reader_adapter_product(T, n_adapters, N, K, r, _ptr(x), _ptr(w), _ptr(base), _ptr(offsets),
+                                            _ptr(rows), _ptr(a), _ptr(b), _ptr(scale), _ptr(y), _ptr(workspace),
+                                            ws_bytes, _stream(stream)))
+
+
+def moe_reader_block_workspace_bytes(B, E, top_e, I, d) -> int:
+    return int(lib().moe_reader_block_workspace_bytes(B, E, top_e, I, d))
+
+
+def moe_reader_forward_grouped(layer: MoeReaderLayer, B, x, residual, y, ids, workspace, ws_bytes, stream=None):
+    _check(lib().moe_reader_forward_grouped(C.byref(layer), B, _ptr(x), _ptr(residual), _ptr(y), _ptr(ids),
+                                            _ptr(workspace), ws_bytes, _stream(stream)))
+
+
 def moe_reader_rmsnorm(B, d, eps, x, h, stream=None):
     _check(lib().moe_reader_rmsnorm(B, d, eps, _ptr(x), _ptr(h), _stream(stream)))
 
@@ -220,6 +287,7 @@ class Layer:
         self.u_sigma = None
         self.v = None
         self._ws = None
+        self._wsg = None
         self.path = 0          # which reader runs a sparse step (see struct)
         self.sketch_format = 0  # 0: 2-bit codes, 1: base 3 (build_sketch(packing=...))
         # [E] int32 weight slot of each expert (held experts only, compacted), or None
@@ -309,7 +377,7 @@ class Layer:
         slot[rank::world] = torch.arange(own.numel(), dtype=torch.int32)
         S.expert_slot = slot.to(dev)
         S.E_held = int(own.numel())
-        S._ws = None
+        S._ws = S._wsg = None
         return S
 
     def workspace(self, B: int):
@@ -368,6 +436,18 @@ class Layer:
         moe_reader_forward_dense(self.struct(0), B, x, residual, y, ws, ws.numel(), stream)
         return y
 
+    def forward_grouped(self, x, residual=None, ids=None, stream=None, out=None):
+        """The all-channel block over any number of tokens (prompts): ids, if
+        given, receives the chosen experts ([B, top_e] int32)."""
+        B = x.shape[0]
+        nb = moe_reader_block_workspace_bytes(B, self.E, self.top_e, self.I, self.d)
+        if self._wsg is None or self._wsg.numel() < nb:
+            self._wsg = torch.zeros(max(nb, 16), dtype=torch.uint8, device=x.device)
+        y = out if out is not None else torch.empty_like(x)
+        moe_reader_forward_grouped(self.struct(0), B, x, residual, y, ids, self._wsg, self._wsg.numel(), stream)
+        return y
+
     def check(self, stream=None):
-        if self._ws is not None:
-            moe_reader_check_error(self._ws, stream)
+        for ws in (self._ws, self._wsg):
+            if ws is not None:
+                moe_reader_check_error(ws, stream)

@@ -35,7 +35,8 @@
  *
  * Limits of this build: 256 <= d <= 4096 and d a power of two;
  * 16 <= I <= 2048; 1 <= k <= c <= I; r in {0, 8, 16, ..., 128} and r <= I;
- * 1 <= top_e <= min(E, 16); E <= 1024; 1 <= B <= 256.
+ * 1 <= top_e <= min(E, 16); E <= 1024; 1 <= B <= 256.  The grouped entry
+ * points (moe_reader_group_rows and below it) state their own limits.
  */
 #ifndef MOE_READER_H
 #define MOE_READER_H
@@ -307,6 +308,103 @@ moe_status moe_reader_forward_host(const moe_reader_layer* layer, int B, int k, 
 moe_status moe_reader_forward_noalloc(const moe_reader_layer* layer, int B, int k, int c,
                                       const uint16_t* x, const uint16_t* residual, uint16_t* y, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Products over ragged groups of rows: the prompt side of a model whose
+ * decode steps the reader serves.  A group is an expert (of (token, slot)
+ * pairs) or an adapter (of tokens); a plan, offsets and rows, says which
+ * rows it has.  One plan serves every product of a step (gate/up, down;
+ * every layer, for adapters).
+ *
+ * Common to these entry points:
+ *  - 1 <= n_groups <= 1024 and 1 <= n_rows <= 1048576.  offsets is DEVICE
+ *    [n_groups + 1] int32: group g holds the sorted positions offsets[g] ..
+ *    offsets[g + 1] - 1; a group may be empty.  Positions from
+ *    offsets[n_groups] on belong to no group: their outputs are left as
+ *    they were.
+ *  - Widths (N, K, d) are multiples of 8 in [8, 32768] and bf16 rows are dense.
+ *  - Products are exact, sums fp32 over the whole length of K, one rounding to
+ *    bf16 at the end.  A row's output does not depend on the other rows.
+ *    Results are the same bits from call to call on the same plan.
+ *  - Plans are checked on the device where they are read: an offset outside
+ *    [0, n_rows] or below the one before it, or a row index outside its
+ *    matrix, records device error bit 8 (moe_reader_check_error:
+ *    MOE_EDEVICE); nothing outside the arrays is read or written, and the
+ *    outputs of that row or group are unusable or left as they were.
+ *  - The workspace rules of moe_reader_forward hold (zero-filled once before
+ *    first use, not shared by calls that may overlap; two captured graphs
+ *    that may run at the same time need two workspaces).  Calls may be
+ *    captured into a graph and replayed.
+ * ------------------------------------------------------------------------ */
+
+/* The plan of n rows with group ids: rows[] = the row numbers 0 .. n-1
+ * sorted by ids (stable: ascending inside a group), offsets as above.  Rows
+ * whose id is outside [0, n_groups) (say -1: no adapter, or an expert held
+ * elsewhere) come behind offsets[n_groups], ascending; that is no error.
+ * ids, rows: DEVICE [n] int32, offsets: DEVICE [n_groups + 1] int32; none may
+ * overlap another. */
+size_t moe_reader_group_workspace_bytes(int n, int n_groups);
+moe_status moe_reader_group_rows(int n, int n_groups, const int32_t* ids, int32_t* offsets, int32_t* rows,
+                                 void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace of the two products below for n_groups groups over n_rows rows. */
+size_t moe_reader_grouped_workspace_bytes(int n_groups, int n_rows);
+
+/* Gate/up of every group with its SwiGLU: for sorted position p of group g
+ *   a[p, i] = silu(x_r . w_gate[g, i, :]) (x_r . w_up[g, i, :]),
+ * r = x_rows[p] / x_div (x_rows NULL: r = p, and x_div must be 1).  With the
+ * pairs (token, slot) of a step as rows and x_div = top_e, x is the tokens
+ * themselves: no permuted copy of them is made.  x [n_x, d], w_gate and w_up
+ * [n_groups, I, d], a [n_rows, I], all bf16; 1 <= I <= 32768 (any I);
+ * 1 <= n_x <= 1048576 (n_x >= n_rows where x_rows is NULL). */
+moe_status moe_reader_grouped_swiglu(int n_groups, int n_rows, int n_x, int I, int d, const uint16_t* x,
+                                     const int32_t* x_rows, int x_div, const int32_t* offsets,
+                                     const uint16_t* w_gate, const uint16_t* w_up, uint16_t* a, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
+/* One product per group: for sorted position p of group g
+ *   y[q, n] = sum_k x[r, k] W_g(n, k),  r as above, q = y_rows[p] (NULL: p).
+ * w_layout 0: w is [n_groups, N, K] (row = output channel, as w_gate);
+ * w_layout 1: w is [n_groups, K, N] (channel-major, as w_down).  x [n_x, K],
+ * y [n_y, N] bf16; 1 <= n_x, n_y <= 1048576.  Rows of y that no position
+ * names are left as they were; a row of y named twice gets one of the two. */
+moe_status moe_reader_grouped_product(int n_groups, int n_rows, int n_x, int n_y, int N, int K, int w_layout,
+                                      const uint16_t* x, const int32_t* x_rows, int x_div, const int32_t* offsets,
+                                      const uint16_t* w, uint16_t* y, const int32_t* y_rows, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
+/* Low-rank adapters of many requests at once, beside a projection that all
+ * share:
+ *   y[t] = base[t] + x[t] W^T + scale_g (x[t] A_g^T) B_g^T,
+ * g = the adapter of token t, of n_adapters; tokens with none get the first
+ * two terms.  offsets and rows: the plan of the T tokens' adapter ids
+ * (moe_reader_group_rows with n = T); rows must name every token once.
+ * x [T, K] bf16; w [N, K] bf16 or NULL (no projection: the adapters beside
+ * something already computed, say the MoE block's output in base); base
+ * [T, N] bf16 or NULL, may be y itself; a [n_adapters, r, K], b [n_adapters,
+ * N, r] bf16; scale [n_adapters] fp32 or NULL (1); y [T, N] bf16.
+ * r in {8, 16, ..., 128}: an adapter of lower rank is padded with zeros.
+ * The low-rank product x A^T keeps 16 significant bits (two bf16 terms). */
+size_t moe_reader_adapter_workspace_bytes(int T, int n_adapters, int K, int N, int r);
+moe_status moe_reader_adapter_product(int T, int n_adapters, int N, int K, int r, const uint16_t* x,
+                                      const uint16_t* w, const uint16_t* base, const int32_t* offsets,
+                                      const int32_t* rows, const uint16_t* a, const uint16_t* b,
+                                      const float* scale, uint16_t* y, void* workspace, size_t ws_bytes,
+                                      void* stream);
+
+/* The all-channel MoE block over any number of tokens (1 <= B <= 32768):
+ * moe_reader_forward_dense's result, for prompts.  Routes every token (the
+ * routing rule of moe_reader_forward), groups the pairs by expert and runs
+ * the two grouped products; the pairs' outputs are summed with their routing
+ * weights in fp32, slot order, `residual` (may be NULL, may be y) added, one
+ * rounding.  The SwiGLU values are rounded to bf16 between the products.
+ * ids: DEVICE [B, top_e] int32, receives the chosen experts; may be NULL.
+ * Reads the router and the three weight matrices of the layer; expert_slot
+ * must be NULL (MOE_EUNSUPPORTED otherwise). */
+size_t moe_reader_block_workspace_bytes(int B, int E, int top_e, int I, int d);
+moe_status moe_reader_forward_grouped(const moe_reader_layer* layer, int B, const uint16_t* x,
+                                      const uint16_t* residual, uint16_t* y, int32_t* ids, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
 /* Between stacked layers: h = bf16(x / sqrt(mean(x^2) + eps)) per token,
  * no learned gain (fp32). */
 moe_status moe_reader_rmsnorm(int B, int d, float eps, const uint16_t* x, uint16_t* h, void* stream);
@@ -323,8 +421,8 @@ moe_status moe_reader_launch_plan(int dense, int B, int E, int top_e, int I, int
  * the current device).  Returns MOE_OK; MOE_ETIMEOUT if a bounded wait ran
  * out since the last check (bit 1); otherwise MOE_EDEVICE for the other
  * device-side checks (bit 2: a work item out of range; bit 4: a routed
- * expert without a weight slot, see moe_reader_layer.expert_slot).  The
- * message names the bits. */
+ * expert without a weight slot, see moe_reader_layer.expert_slot; bit 8: a
+ * group plan out of range).  The message names the bits. */
 moe_status moe_reader_check_error(void* workspace, void* stream);
 
 /* Message for the last non-OK status returned on this thread. */
