@@ -463,6 +463,8 @@ moe_status moe_reader_grouped_swiglu(int n_groups, int n_rows, int n_x, int I, i
   g.w = w_gate;
   g.w_up = w_up;
   g.y = a;
+  g.ldx = d;
+  g.ldy = I;
   g.err = static_cast<uint32_t*>(workspace);
   cudaError_t e = moe::launch_grouped(g, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "grouped_swiglu launch");
@@ -501,6 +503,8 @@ moe_status moe_reader_grouped_product(int n_groups, int n_rows, int n_x, int n_y
   g.offsets = offsets;
   g.w = w;
   g.y = y;
+  g.ldx = K;
+  g.ldy = N;
   g.y_rows = y_rows;
   g.err = static_cast<uint32_t*>(workspace);
   cudaError_t e = moe::launch_grouped(g, static_cast<cudaStream_t>(stream));

@@ -99,6 +99,9 @@ __global__ void __launch_bounds__(256) combine_kernel(BlockArgs a) {
   }
 }
 
+// row stride of the SwiGLU values: bulk copies want 16-byte rows
+int lda(int I) { return (I + 7) / 8 * 8; }
+
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
@@ -113,7 +116,7 @@ size_t block_layout(int B, int E, int top_e, int I, int d, void* base, BlockArgs
   };
   const size_t o_err = take(16), o_log = take(sizeof(double) * B * E), o_ids = take(sizeof(int32_t) * P),
                o_w = take(sizeof(float) * P), o_off = take(sizeof(int32_t) * (E + 1)),
-               o_rows = take(sizeof(int32_t) * P), o_a = take(sizeof(uint16_t) * P * I),
+               o_rows = take(sizeof(int32_t) * P), o_a = take(sizeof(uint16_t) * P * lda(I)),
                o_out = take(sizeof(float) * P * d);
   if (base && a) {
     char* p = static_cast<char*>(base);
@@ -151,6 +154,8 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
   g.w = a.w_gate;
   g.w_up = a.w_up;
   g.y = a.a;
+  g.ldx = a.d;
+  g.ldy = lda(a.I);
   g.err = a.err;
   e = launch_grouped(g, s);
   if (e != cudaSuccess) return e;
@@ -167,6 +172,8 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
   h.offsets = a.offsets;
   h.w = a.w_down;
   h.y = a.out;
+  h.ldx = lda(a.I);
+  h.ldy = a.d;
   h.y_fp32 = 1;
   h.y_rows = a.rows;
   h.err = a.err;

@@ -160,6 +160,7 @@ cudaError_t launch_group_rows(int n, int n_groups, const int32_t* ids, int32_t* 
 
 struct GroupedArgs {
   int G, P, n_x, n_y, N, K;
+  int ldx, ldy;             // row strides of x (a multiple of 8) and y, in elements
   int layout;               // 0: w [G, N, K]; 1: w [G, K, N]
   const uint16_t* x;        // [n_x, K]
   const int32_t* x_rows;    // [P] or null
@@ -207,7 +208,7 @@ struct BlockArgs {
   float* wts;         // [B, top_e]
   int32_t* offsets;   // [E + 1]
   int32_t* rows;      // [B * top_e]
-  uint16_t* a;        // [B * top_e, I]
+  uint16_t* a;        // [B * top_e, I rounded up to 8]
   float* out;         // [B * top_e, d]
 };
 size_t block_layout(int B, int E, int top_e, int I, int d, void* base, BlockArgs* a);

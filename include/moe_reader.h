@@ -328,8 +328,9 @@ moe_status moe_reader_forward_noalloc(const moe_reader_layer* layer, int B, int 
  *  - Plans are checked on the device where they are read: an offset outside
  *    [0, n_rows] or below the one before it, or a row index outside its
  *    matrix, records device error bit 8 (moe_reader_check_error:
- *    MOE_EDEVICE); nothing outside the arrays is read or written, and the
- *    outputs of that row or group are unusable or left as they were.
+ *    MOE_EDEVICE); nothing outside the arrays is read or written.  A bad
+ *    row's output is left as it was or unusable; with bad offsets the whole
+ *    call's are.
  *  - The workspace rules of moe_reader_forward hold (zero-filled once before
  *    first use, not shared by calls that may overlap; two captured graphs
  *    that may run at the same time need two workspaces).  Calls may be
