@@ -34,6 +34,13 @@ __device__ __forceinline__ uint16_t f2bf16(float f) {
   return (uint16_t)(u >> 16);
 }
 
+// Two fp32 -> two bf16 in a word (lo in the low half), round to nearest even.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // ------------------------------------------------------------ exp / SiLU
 // exp_r: Cody & Waite reduction t = n ln2 + r (ln 2 split into a
 // 16-significant-bit head and an fp32 tail), degree-7 Taylor polynomial of

@@ -2,19 +2,25 @@
 // prompts, per-request adapters) on the tensor cores.
 //
 // D[channel, row] = sum_k W_g[channel, k] x[row, k]: the weights are the A
-// operand (128 channels, the lanes of the accumulator), the rows of a group
+// operand (channels are the lanes of the accumulator), the rows of a group
 // the B operand (its columns).  The groups are ragged, and a column count may
-// be any multiple of 16, so a tile pads a group by 15 rows at most; with the
-// rows as lanes it would pad by up to 127.  For SwiGLU the 32 lanes of each
-// warp hold 16 gate and the 16 up channels they belong with, so that a value
-// and its gate meet in one shuffle.
+// be any multiple of 32, so a tile pads a group by 31 rows at most; with the
+// rows as lanes it would pad by up to 255.
 //
-// One CTA per SM walks the tiles (group, rows, channels).  Warp 0 fills a
-// ring of shared-memory stages by bulk tensor copies (weights in boxes, rows
-// in boxes or gathered four at a time through the plan's row list), one
-// thread of warp 1 issues the products, warps 4 .. 7 read the accumulator
-// back, transform and store; two accumulators let that overlap the next
-// tile's products.
+// A pair of CTAs works on 256 channels by up to 256 rows: each CTA holds the
+// operands of its own 128 channels and of half of the rows, which halves what
+// a CTA has to fetch for the rows (32 KB instead of 48 KB for 128 x 256 x 64
+// multiply-adds).  The pairs walk the tiles (group, rows, channels).  In each CTA
+// warp 0 fetches boxes by bulk tensor copies into a ring of stages; warps
+// 8 .. 11 fetch the rows where they are gathered through the plan's row list
+// (16-byte copies; gathering bulk copies move four rows in about 80 cycles,
+// a third of the rate that the products need); one thread of the pair's first CTA issues the
+// products; warps 4 .. 7 read the accumulator back, transform and store.  Two
+// accumulators let that overlap the next tile's products.
+//
+// For SwiGLU a CTA's 128 lanes are 64 gate and the same 64 up channels; the
+// warps of a gate and an up quarter swap half of their columns through shared
+// memory.
 #include <cudaTypedefs.h>
 
 #include "kernels.h"
@@ -44,24 +50,25 @@ bool tensor_map(CUtensorMap* m, const void* base, uint64_t x, uint64_t y, uint64
 
 namespace {
 
-constexpr int kGThreads = 256;
-constexpr int kLanes = 128;                // channels per tile (gate and up together)
+constexpr int kGThreads = 384;
+constexpr int kLanes = 128;                // channels per CTA (gate and up together)
 constexpr int kBlockK = 64;                // K per stage: one 128-byte swizzled row
 constexpr int kMaxCols = 256;              // rows per tile
 constexpr int kABytes = kLanes * kBlockK * 2;
 constexpr int kMaxStages = 8;
-constexpr int kBoxRows = 32;               // rows per box of an ungathered x
+constexpr int kRowBoxes = 4;               // boxes of 128, 64, 32 and 16 rows
 constexpr int kSmemBudget = 227 * 1024 - 1024;  // 1024: the ring's alignment
 
 struct Maps {
-  CUtensorMap x, w, w_up;
+  CUtensorMap x[kRowBoxes], w, w_up;
 };
 
 struct TileArgs {
-  int G, P, n_x, n_y, N, K, ldy;
+  int G, P, n_x, n_y, N, K, ldx, ldy;
   int cols;      // rows per tile at most (multiple of 32)
   int stages, stage_bytes;
   int layout, gather, x_div, y_fp32;
+  const uint16_t* x;
   const int32_t* x_rows;
   const int32_t* offsets;
   const int32_t* y_rows;
@@ -71,20 +78,21 @@ struct TileArgs {
 
 // Shared memory behind the ring.
 struct Side {
-  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+  uint64_t full[kMaxStages], landed[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int stop, tiles;
   int scan[kGThreads / 32];
-  int y_row[kMaxCols];
-  int first[kMaxGroups];       // first sorted position of each group
-  int rows[kMaxGroups];        // rows of each group
-  int before[kMaxGroups + 1];  // row tiles of the groups before
+  alignas(16) int y_row[kMaxCols];  // result row of each column, -1: none; even columns, then odd ones
+  float swap[2][2][2][16][32];      // [quarter][turn][from the up side][column][lane]
+  int first[kMaxGroups];            // first sorted position of each group
+  int rows[kMaxGroups];             // rows of each group
+  int before[kMaxGroups + 1];       // row tiles of the groups before
 };
 
 // Checks the plan and lays its groups out as row tiles; every thread of the CTA.
 __device__ void lay_tiles(const TileArgs& a, Side& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kPer = kMaxGroups / kGThreads;
+  constexpr int kPer = (kMaxGroups + kGThreads - 1) / kGThreads;
   int n[kPer], t[kPer], sum = 0;
   bool bad = false;
 #pragma unroll
@@ -140,9 +148,9 @@ __device__ __forceinline__ Tile tile_of(const TileArgs& a, const Side& s, int u,
     else
       hi = m - 1;
   }
-  // a group's row tiles are as even as steps of 16 allow
+  // a group's row tiles are as even as steps of 32 allow
   const int rows = s.rows[lo], nt = (rows + a.cols - 1) / a.cols;
-  const int size = ((rows + nt - 1) / nt + 15) & ~15, at = (q - s.before[lo]) * size;
+  const int size = ((rows + nt - 1) / nt + 31) & ~31, at = (q - s.before[lo]) * size;
   Tile t;
   t.g = lo;
   t.p0 = s.first[lo] + at;
@@ -151,26 +159,86 @@ __device__ __forceinline__ Tile tile_of(const TileArgs& a, const Side& s, int u,
   return t;
 }
 
+// The rows of x at sorted positions, gathered: thread i of 128 copies the
+// 16-byte piece i % 8 of rows i / 8 + 16 m of this CTA's half of the tile.  A
+// stage's copies arrive on landed[stage] as they complete; warp 3 passes that
+// on to the issuing CTA, so that the copying threads never wait for their copies.
+__device__ void gather_rows(const TileArgs& a, Side& s, uint8_t* ring, int units, int n_ct, int nkb, int rank) {
+  const int t = threadIdx.x - 256, piece = t & 7, r0 = t >> 3;
+  volatile int* stop = &s.stop;
+  int it = 0;
+  bool ok = true;
+  for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
+    const Tile tl = tile_of(a, s, u, n_ct);
+    const int half = ((tl.n + 31) & ~31) >> 1;
+    const uint16_t* src[8];
+#pragma unroll
+    for (int m = 0; m < 8; m++) {
+      // rows past the tile's end repeat its last one (their columns are not stored)
+      int row = 0;
+      if (r0 + 16 * m < half) {
+        row = a.x_rows[tl.p0 + min(rank * half + r0 + 16 * m, tl.n - 1)];
+        row = row < 0 ? -1 : row / a.x_div;
+        if (row < 0 || row >= a.n_x) {
+          atomicOr(a.err, kErrBadPlan);
+          row = 0;
+        }
+      }
+      src[m] = a.x + (size_t)row * a.ldx + piece * 8;
+    }
+    for (int kb = 0; kb < nkb; kb++, it++) {
+      const int st = it % a.stages;
+      ok = wait_or_stop(&s.empty[st], ((it / a.stages) & 1) ^ 1, stop, a.err);
+      if (__any_sync(0xffffffffu, !ok)) {
+        ok = false;
+        break;
+      }
+      const uint32_t dst = smem_u32(ring + (size_t)st * a.stage_bytes + kABytes) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
+      const bool in = kb * kBlockK + piece * 8 < a.K;
+#pragma unroll
+      for (int m = 0; m < 8; m++)
+        if (r0 + 16 * m < half) cp_async16(dst + m * 2048, in ? src[m] + kb * kBlockK : a.x, in);
+      cp_async_arrive(&s.landed[st]);
+    }
+  }
+  cp_async_wait_all();
+}
+
+// Passes each stage of gathered rows on: complete here, made visible to the
+// tensor cores, announced to the issuing CTA.
+__device__ void announce_rows(const TileArgs& a, Side& s, int units, int nkb) {
+  const uint32_t full = peer_u32(s.full, 0);
+  for (int u = blockIdx.x >> 1, it = 0; u < units; u += gridDim.x >> 1)
+    for (int kb = 0; kb < nkb; kb++, it++) {
+      const int st = it % a.stages;
+      if (!wait_or_stop(&s.landed[st], (it / a.stages) & 1, &s.stop, a.err)) return;
+      fence_proxy_async();
+      mbar_arrive_at(full + st * 8);
+    }
+}
+
 template <bool kSwiglu>
-__global__ void __launch_bounds__(kGThreads, 1) tiles_kernel(const __grid_constant__ Maps maps, const TileArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
+    tiles_kernel(const __grid_constant__ Maps maps, const TileArgs a) {
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   Side& s = *reinterpret_cast<Side*>(ring + (size_t)a.stages * a.stage_bytes);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kChan = kSwiglu ? kLanes / 2 : kLanes;  // output channels per tile
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x & 1;
+  constexpr int kChan = kSwiglu ? kLanes / 2 : kLanes;  // output channels per CTA
   if (tid == 0) {
     for (int i = 0; i < a.stages; i++) {
-      mbar_init(&s.full[i], 1);
+      mbar_init(&s.full[i], a.gather ? 3 : 1);  // the boxes' announcement, and the gathered rows' of each CTA
+      mbar_init(&s.landed[i], 128);
       mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < 2; i++) {
       mbar_init(&s.acc_full[i], 1);
-      mbar_init(&s.acc_empty[i], 4);
+      mbar_init(&s.acc_empty[i], 8);  // four warps of each CTA
     }
     mbar_init(&s.drain, 1);
     s.stop = 0;
     fence_mbar_init();
-    tma_prefetch(&maps.x);
+    for (int i = 0; i < kRowBoxes; i++) tma_prefetch(&maps.x[i]);
     tma_prefetch(&maps.w);
     if (kSwiglu) tma_prefetch(&maps.w_up);
   }
@@ -179,85 +247,65 @@ __global__ void __launch_bounds__(kGThreads, 1) tiles_kernel(const __grid_consta
   pdl_wait();
   tc_fence_before();
   lay_tiles(a, s);
+  cluster_arrive();
+  cluster_wait();  // the pair's barriers are ready
   tc_fence_after();
   const uint32_t tmem = s.tmem;
-  const int n_ct = (a.N + kChan - 1) / kChan, units = s.tiles * n_ct, nkb = (a.K + kBlockK - 1) / kBlockK;
+  const int n_ct = (a.N + 2 * kChan - 1) / (2 * kChan), units = s.tiles * n_ct, nkb = (a.K + kBlockK - 1) / kBlockK;
+  const int u0 = blockIdx.x >> 1, du = gridDim.x >> 1;
   volatile int* stop = &s.stop;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- copies
+  if (warp == 0 && lane == 0) {
+    // ----------------------------------------------------------- boxes
     int it = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    for (int u = u0; u < units && ok; u += du) {
       const Tile t = tile_of(a, s, u, n_ct);
-      const int quads = (t.n + 15) / 16 * 4, boxes = (t.n + kBoxRows - 1) / kBoxRows;
-      const uint32_t bytes = kABytes + (a.gather ? quads * 4 : boxes * kBoxRows) * 128;
-      int r[2][4];
-      if (a.gather) {
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            // rows past the tile's end repeat its last one (their columns are not stored)
-            const int j = min((lane + 32 * h) * 4 + i, t.n - 1);
-            int row = a.x_rows[t.p0 + j];
-            row = row < 0 ? -1 : row / a.x_div;
-            if (row < 0 || row >= a.n_x) {
-              atomicOr(a.err, kErrBadPlan);
-              row = 0;
-            }
-            r[h][i] = row;
-          }
-      }
+      const int half = ((t.n + 31) & ~31) >> 1, c0 = (t.c0 * 2 + rank) * kChan;
+      const uint32_t bytes = 2 * (kABytes + (a.gather ? 0 : half * 128));  // of both CTAs
       for (int kb = 0; kb < nkb; kb++, it++) {
         const int st = it % a.stages;
         ok = wait_or_stop(&s.empty[st], ((it / a.stages) & 1) ^ 1, stop, a.err);
-        if (__any_sync(0xffffffffu, !ok)) {
-          ok = false;
-          break;
-        }
+        if (!ok) break;
         uint8_t* A = ring + (size_t)st * a.stage_bytes;
         uint8_t* B = A + kABytes;
         const int k0 = kb * kBlockK;
-        if (lane == 0) {
-          mbar_expect_tx(&s.full[st], bytes);
-          if (kSwiglu) {
+        const uint32_t bar = peer_u32(&s.full[st], 0);
+        if (rank == 0) mbar_expect_tx(&s.full[st], bytes);
+        if (kSwiglu) {
+          tma_3d(A, &maps.w, k0, c0, t.g, bar);
+          tma_3d(A + kABytes / 2, &maps.w_up, k0, c0, t.g, bar);
+        } else if (a.layout) {
+          tma_3d(A, &maps.w, c0, k0, t.g, bar);
+          tma_3d(A + kABytes / 2, &maps.w, c0 + 64, k0, t.g, bar);
+        } else {
+          tma_3d(A, &maps.w, k0, c0, t.g, bar);
+        }
+        if (!a.gather) {
+          int at = 0;
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-              tma_3d(A + q * 4096, &maps.w, k0, t.c0 * kChan + q * 16, t.g, &s.full[st]);
-              tma_3d(A + q * 4096 + 2048, &maps.w_up, k0, t.c0 * kChan + q * 16, t.g, &s.full[st]);
+          for (int b = 0; b < kRowBoxes; b++) {
+            const int h = 128 >> b;
+            if (half & h) {
+              tma_2d(B + at * 128, &maps.x[b], k0, t.p0 + rank * half + at, bar);
+              at += h;
             }
-          } else if (a.layout) {
-            tma_3d(A, &maps.w, t.c0 * kChan, k0, t.g, &s.full[st]);
-            tma_3d(A + kABytes / 2, &maps.w, t.c0 * kChan + 64, k0, t.g, &s.full[st]);
-          } else {
-            tma_3d(A, &maps.w, k0, t.c0 * kChan, t.g, &s.full[st]);
           }
-          if (!a.gather)
-            for (int b = 0; b < boxes; b++)
-              tma_2d(B + b * kBoxRows * 128, &maps.x, k0, t.p0 + b * kBoxRows, &s.full[st]);
         }
-        __syncwarp();
-        if (a.gather) {
-#pragma unroll
-          for (int h = 0; h < 2; h++)
-            if (lane + 32 * h < quads) tma_gather4(B + (lane + 32 * h) * 512, &maps.x, k0, r[h], &s.full[st]);
-        }
-        __syncwarp();
       }
     }
-    // after a timeout: the copies in flight must land before the CTA ends
-    if (!ok && lane == 0)
+    // after a timeout: the copies in flight must land before the pair ends
+    if (!ok && rank == 0)
       for (int i = it > a.stages ? it - a.stages : 0; i < it; i++)
         mbar_wait_bounded(&s.full[i % a.stages], (i / a.stages) & 1, a.err);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1 && lane == 0 && rank == 0) {
     // -------------------------------------------------------- products
     int it = 0, ti = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ti++) {
+    for (int u = u0; u < units && ok; u += du, ti++) {
       const Tile t = tile_of(a, s, u, n_ct);
       const uint32_t d = tmem + (ti & 1) * kMaxCols;
-      const uint32_t idesc = mma_desc(kLanes, (t.n + 15) & ~15, !kSwiglu && a.layout);
+      const uint32_t idesc = mma_desc(2 * kLanes, (t.n + 31) & ~31, !kSwiglu && a.layout);
       ok = wait_or_stop(&s.acc_empty[ti & 1], ((ti >> 1) & 1) ^ 1, stop, a.err);
       if (!ok) break;
       tc_fence_after();
@@ -268,7 +316,7 @@ __global__ void __launch_bounds__(kGThreads, 1) tiles_kernel(const __grid_consta
         tc_fence_after();
         const uint32_t A = smem_u32(ring + (size_t)st * a.stage_bytes);
         const uint64_t bd = tile_desc(A + kABytes, 16);
-        const int steps = min(kBlockK, a.K - kb * kBlockK + 15) / 16;  // past K the stage holds zeros
+        const int steps = (min(kBlockK, a.K - kb * kBlockK) + 15) / 16;  // past K the stage holds zeros
         if (!kSwiglu && a.layout) {
           const uint64_t ad = tile_desc(A, kABytes / 2);
           for (int k = 0; k < steps; k++) mma_bf16(d, ad + k * (2048 >> 4), bd + k * 2, idesc, kb + k > 0);
@@ -280,27 +328,35 @@ __global__ void __launch_bounds__(kGThreads, 1) tiles_kernel(const __grid_consta
       }
       if (ok) mma_commit(&s.acc_full[ti & 1]);
     }
-    if (!ok) {  // after a timeout: the products in flight must end before the CTA does
+    if (!ok) {  // after a timeout: the products in flight must end before the pair does
       mma_commit(&s.drain);
       mbar_wait_bounded(&s.drain, 0, a.err);
     }
+  } else if (warp == 3 && lane == 0) {
+    if (a.gather) announce_rows(a, s, units, nkb);
+  } else if (warp >= 8) {
+    if (a.gather) gather_rows(a, s, ring, units, n_ct, nkb, rank);
   } else if (warp >= 4) {
     // ------------------------------------------------- read back, store
     const int q4 = warp - 4, et = tid - 128;
-    int ti = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ti++) {
+    const bool odd = lane & 1;
+    int ti = 0, turn = 0;
+    for (int u = u0; u < units; u += du, ti++) {
       const Tile t = tile_of(a, s, u, n_ct);
-      for (int j = et; j < t.n; j += 128) {
-        int q = a.y_rows ? a.y_rows[t.p0 + j] : t.p0 + j;
-        if (q < 0 || q >= a.n_y) {
-          atomicOr(a.err, kErrBadPlan);
-          q = -1;
+      for (int j = et; j < ((t.n + 31) & ~31); j += 128) {
+        int q = -1;
+        if (j < t.n) {
+          q = a.y_rows ? a.y_rows[t.p0 + j] : t.p0 + j;
+          if (q < 0 || q >= a.n_y) {
+            atomicOr(a.err, kErrBadPlan);
+            q = -1;
+          }
+          if (a.gather) {  // a row that is not there has no result
+            const int row = a.x_rows[t.p0 + j];
+            if (row < 0 || row / a.x_div >= a.n_x) q = -1;
+          }
         }
-        if (a.gather) {  // a row that is not there has no result
-          const int row = a.x_rows[t.p0 + j];
-          if (row < 0 || row / a.x_div >= a.n_x) q = -1;
-        }
-        s.y_row[j] = q;
+        s.y_row[(j & 1) * (kMaxCols / 2) + (j >> 1)] = q;
       }
       const bool ok = wait_or_stop(&s.acc_full[ti & 1], (ti >> 1) & 1, stop, a.err);
       if (bar_any(1, 128, !ok)) break;
@@ -310,54 +366,81 @@ __global__ void __launch_bounds__(kGThreads, 1) tiles_kernel(const __grid_consta
         float v[32];
         tmem_ld32(acc + j0, v);
         if (kSwiglu) {
-          // lanes 0..15 hold the gates, 16..31 the ups of channels c: the lower
-          // half finishes the even column of a pair, the upper half the odd one
-          const int c = t.c0 * kChan + q4 * 16 + (lane & 15);
-          const bool up = lane >= 16;
+          // the gate side finishes the even columns, the up side the odd ones
+          const bool up = q4 >= 2;
+          float(&out)[16][32] = s.swap[q4 & 1][turn][up ? 1 : 0];
+          float(&in)[16][32] = s.swap[q4 & 1][turn][up ? 0 : 1];
+          turn ^= 1;
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float o = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 16);
-            const float g = up ? o : v[j], w = up ? v[j + 1] : o;
-            const int jj = j0 + j + (up ? 1 : 0);
-            if (jj < t.n && c < a.N) {
-              const int q = s.y_row[jj];
-              if (q >= 0)
-                static_cast<uint16_t*>(a.y)[(size_t)q * a.ldy + c] = f2bf16(__fdividef(g, 1.0f + __expf(-g)) * w);
+          for (int i = 0; i < 16; i++) out[i][lane] = up ? v[2 * i] : v[2 * i + 1];
+          bar_any(2 + (q4 & 1), 64, false);
+          float r[16];
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            const float o = in[i][lane], g = up ? o : v[2 * i], w = up ? v[2 * i + 1] : o;
+            r[i] = __fdividef(g, 1.0f + __expf(-g)) * w;
+          }
+          const int* q_of = s.y_row + (up ? kMaxCols / 2 : 0) + (j0 >> 1);
+          const int cw = (t.c0 * 2 + rank) * kChan + (q4 & 1) * 32;
+          uint16_t* y = static_cast<uint16_t*>(a.y);
+          if (a.ldy & 1) {  // rows that start on odd words
+            const int c = cw + lane;
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+              const int q = q_of[i];
+              if (q >= 0 && c < a.N) y[(size_t)q * a.ldy + c] = f2bf16(r[i]);
+            }
+          } else {
+            const int c = cw + (lane & ~1);
+            if (c < a.N) y += c;
+            const bool in_n = c < a.N;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float o = __shfl_xor_sync(0xffffffffu, odd ? r[i] : r[i + 1], 1);
+              const uint32_t w = odd ? bf16x2(o, r[i + 1]) : bf16x2(r[i], o);
+              const int q = q_of[i + (odd ? 1 : 0)];
+              if (q >= 0 && in_n) *reinterpret_cast<uint32_t*>(y + (size_t)q * a.ldy) = w;
             }
           }
         } else if (a.y_fp32) {
-          const int c = t.c0 * kChan + q4 * 32 + lane;
+          const int c = (t.c0 * 2 + rank) * kChan + q4 * 32 + lane;
+          const bool in_n = c < a.N;
+          float* y = static_cast<float*>(a.y) + c;
 #pragma unroll
-          for (int j = 0; j < 32; j++)
-            if (j0 + j < t.n && c < a.N) {
-              const int q = s.y_row[j0 + j];
-              if (q >= 0) static_cast<float*>(a.y)[(size_t)q * a.ldy + c] = v[j];
-            }
+          for (int j = 0; j < 32; j++) {
+            const int q = s.y_row[(j & 1) * (kMaxCols / 2) + ((j0 + j) >> 1)];
+            if (q >= 0 && in_n) y[(size_t)q * a.ldy] = v[j];
+          }
         } else {
           // two channels to a word: the even lane of a pair takes the even column
-          const int c = t.c0 * kChan + q4 * 32 + (lane & ~1);
-          const bool odd = lane & 1;
+          const int c = (t.c0 * 2 + rank) * kChan + q4 * 32 + (lane & ~1);
+          const bool in_n = c < a.N;
+          uint16_t* y = static_cast<uint16_t*>(a.y) + c;
+          const int4* q_of = reinterpret_cast<const int4*>(s.y_row + (odd ? kMaxCols / 2 : 0) + (j0 >> 1));
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float o = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-            const uint32_t w = odd ? f2bf16(o) | ((uint32_t)f2bf16(v[j + 1]) << 16)
-                                   : f2bf16(v[j]) | ((uint32_t)f2bf16(o) << 16);
-            const int jj = j0 + j + (odd ? 1 : 0);
-            if (jj < t.n && c < a.N) {
-              const int q = s.y_row[jj];
-              if (q >= 0) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.y) + (size_t)q * a.ldy + c) = w;
+          for (int i = 0; i < 4; i++) {
+            const int4 q = q_of[i];
+            const int qs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+              const int j = 8 * i + 2 * k;
+              const float o = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+              const uint32_t w = odd ? bf16x2(o, v[j + 1]) : bf16x2(v[j], o);
+              if (qs[k] >= 0 && in_n) *reinterpret_cast<uint32_t*>(y + (size_t)qs[k] * a.ldy) = w;
             }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.acc_empty[ti & 1]);
+      if (lane == 0) mbar_arrive_at(peer_u32(&s.acc_empty[ti & 1], 0));
       bar_any(1, 128, false);  // y_row is rewritten for the next tile
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_arrive();
+  cluster_wait();  // neither CTA leaves while the other may still signal it
   if (warp == 2) tmem_free(tmem, 512);
 }
 
@@ -413,7 +496,7 @@ int sm_count() {
 
 template <bool kSwiglu>
 cudaError_t run_tiles(const Maps& m, TileArgs t, cudaStream_t s) {
-  t.stage_bytes = kABytes + t.cols * 128;
+  t.stage_bytes = kABytes + t.cols / 2 * 128;
   t.stages = (kSmemBudget - (int)sizeof(Side)) / t.stage_bytes;
   if (t.stages > kMaxStages) t.stages = kMaxStages;
   const size_t smem = 1024 + (size_t)t.stages * t.stage_bytes + sizeof(Side);
@@ -421,10 +504,10 @@ cudaError_t run_tiles(const Maps& m, TileArgs t, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const int chan = kSwiglu ? kLanes / 2 : kLanes, n_ct = (t.N + chan - 1) / chan;
+  const int chan = kSwiglu ? kLanes : 2 * kLanes, n_ct = (t.N + chan - 1) / chan;
   const long most = ((long)(t.P + t.cols - 1) / t.cols + (t.G < t.P ? t.G : t.P)) * n_ct;  // units at most
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+  cfg.gridDim = dim3((unsigned)(2 * (most < sms / 2 ? most : sms / 2)));
   cfg.blockDim = dim3(kGThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -457,12 +540,16 @@ cudaError_t launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   t.y = a.y;
   t.err = a.err;
   t.cols = a.P < kMaxCols ? (a.P + 31) / 32 * 32 : kMaxCols;
+  t.x = a.x;
+  t.ldx = a.ldx;
   Maps m;
   const uint64_t N = a.N, K = a.K;
-  bool ok = tensor_map(&m.x, a.x, K, a.n_x, 0, 2ull * a.ldx, 0, kBlockK, t.gather ? 1 : kBoxRows);
+  bool ok = true;
+  for (int b = 0; b < kRowBoxes; b++)
+    ok = ok && tensor_map(&m.x[b], a.x, K, a.n_x, 0, 2ull * a.ldx, 0, kBlockK, 128 >> b);
   if (a.w_up) {
-    ok = ok && tensor_map(&m.w, a.w, K, N, a.G, 2 * K, 2 * N * K, kBlockK, 16) &&
-         tensor_map(&m.w_up, a.w_up, K, N, a.G, 2 * K, 2 * N * K, kBlockK, 16);
+    ok = ok && tensor_map(&m.w, a.w, K, N, a.G, 2 * K, 2 * N * K, kBlockK, kLanes / 2) &&
+         tensor_map(&m.w_up, a.w_up, K, N, a.G, 2 * K, 2 * N * K, kBlockK, kLanes / 2);
   } else {
     ok = ok && (a.layout ? tensor_map(&m.w, a.w, N, K, a.G, 2 * N, 2 * N * K, 64, kBlockK)
                          : tensor_map(&m.w, a.w, K, N, a.G, 2 * K, 2 * N * K, kBlockK, kLanes));
