@@ -89,6 +89,17 @@ struct Side {
   int before[kMaxGroups + 1];       // row tiles of the groups before
 };
 
+// A role's place in the ring: the stage, and how often it has gone round.
+struct Turn {
+  int st = 0, round = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++st == stages) {
+      st = 0;
+      round ^= 1;
+    }
+  }
+};
+
 // Checks the plan and lays its groups out as row tiles; every thread of the CTA.
 __device__ void lay_tiles(const TileArgs& a, Side& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -166,7 +177,7 @@ __device__ __forceinline__ Tile tile_of(const TileArgs& a, const Side& s, int u,
 __device__ void gather_rows(const TileArgs& a, Side& s, uint8_t* ring, int units, int n_ct, int nkb, int rank) {
   const int t = threadIdx.x - 256, piece = t & 7, r0 = t >> 3;
   volatile int* stop = &s.stop;
-  int it = 0;
+  Turn it;
   bool ok = true;
   for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
     const Tile tl = tile_of(a, s, u, n_ct);
@@ -186,9 +197,9 @@ __device__ void gather_rows(const TileArgs& a, Side& s, uint8_t* ring, int units
       }
       src[m] = a.x + (size_t)row * a.ldx + piece * 8;
     }
-    for (int kb = 0; kb < nkb; kb++, it++) {
-      const int st = it % a.stages;
-      ok = wait_or_stop(&s.empty[st], ((it / a.stages) & 1) ^ 1, stop, a.err);
+    for (int kb = 0; kb < nkb; kb++, it.next(a.stages)) {
+      const int st = it.st;
+      ok = wait_or_stop(&s.empty[st], it.round ^ 1, stop, a.err);
       if (__any_sync(0xffffffffu, !ok)) {
         ok = false;
         break;
@@ -208,12 +219,12 @@ __device__ void gather_rows(const TileArgs& a, Side& s, uint8_t* ring, int units
 // tensor cores, announced to the issuing CTA.
 __device__ void announce_rows(const TileArgs& a, Side& s, int units, int nkb) {
   const uint32_t full = peer_u32(s.full, 0);
-  for (int u = blockIdx.x >> 1, it = 0; u < units; u += gridDim.x >> 1)
-    for (int kb = 0; kb < nkb; kb++, it++) {
-      const int st = it % a.stages;
-      if (!wait_or_stop(&s.landed[st], (it / a.stages) & 1, &s.stop, a.err)) return;
+  Turn it;
+  for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1)
+    for (int kb = 0; kb < nkb; kb++, it.next(a.stages)) {
+      if (!wait_or_stop(&s.landed[it.st], it.round, &s.stop, a.err)) return;
       fence_proxy_async();
-      mbar_arrive_at(full + st * 8);
+      mbar_arrive_at(full + it.st * 8);
     }
 }
 
@@ -255,23 +266,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   const int u0 = blockIdx.x >> 1, du = gridDim.x >> 1;
   volatile int* stop = &s.stop;
 
-  if (warp == 0 && lane == 0) {
-    // ----------------------------------------------------------- boxes
-    int it = 0;
+  if ((warp == 0 || (warp == 2 && !a.gather)) && lane == 0) {
+    // ----------------------- boxes: the weights (warp 0), the rows (warp 2)
+    const bool rows = warp == 2;
+    Turn it;
+    int filled = 0;
     bool ok = true;
+    const uint32_t full = peer_u32(s.full, 0);
     for (int u = u0; u < units && ok; u += du) {
       const Tile t = tile_of(a, s, u, n_ct);
-      const int half = ((t.n + 31) & ~31) >> 1, c0 = (t.c0 * 2 + rank) * kChan;
+      const int half = ((t.n + 31) & ~31) >> 1, c0 = (t.c0 * 2 + rank) * kChan, p = t.p0 + rank * half;
       const uint32_t bytes = 2 * (kABytes + (a.gather ? 0 : half * 128));  // of both CTAs
-      for (int kb = 0; kb < nkb; kb++, it++) {
-        const int st = it % a.stages;
-        ok = wait_or_stop(&s.empty[st], ((it / a.stages) & 1) ^ 1, stop, a.err);
+      for (int k0 = 0; k0 < a.K; k0 += kBlockK, it.next(a.stages), filled++) {
+        ok = wait_or_stop(&s.empty[it.st], it.round ^ 1, stop, a.err);
         if (!ok) break;
-        uint8_t* A = ring + (size_t)st * a.stage_bytes;
-        uint8_t* B = A + kABytes;
-        const int k0 = kb * kBlockK;
-        const uint32_t bar = peer_u32(&s.full[st], 0);
-        if (rank == 0) mbar_expect_tx(&s.full[st], bytes);
+        uint8_t* A = ring + (size_t)it.st * a.stage_bytes;
+        const uint32_t bar = full + it.st * 8;
+        if (rows) {
+          uint8_t* B = A + kABytes;
+          if (half == 128) {
+            tma_2d(B, &maps.x[0], k0, p, bar);
+          } else {
+            int at = 0;
+#pragma unroll
+            for (int b = 1; b < kRowBoxes; b++) {
+              const int h = 128 >> b;
+              if (half & h) {
+                tma_2d(B + at * 128, &maps.x[b], k0, p + at, bar);
+                at += h;
+              }
+            }
+          }
+          continue;
+        }
+        if (rank == 0) mbar_expect_tx(&s.full[it.st], bytes);
         if (kSwiglu) {
           tma_3d(A, &maps.w, k0, c0, t.g, bar);
           tma_3d(A + kABytes / 2, &maps.w_up, k0, c0, t.g, bar);
@@ -281,26 +309,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         } else {
           tma_3d(A, &maps.w, k0, c0, t.g, bar);
         }
-        if (!a.gather) {
-          int at = 0;
-#pragma unroll
-          for (int b = 0; b < kRowBoxes; b++) {
-            const int h = 128 >> b;
-            if (half & h) {
-              tma_2d(B + at * 128, &maps.x[b], k0, t.p0 + rank * half + at, bar);
-              at += h;
-            }
-          }
-        }
       }
     }
     // after a timeout: the copies in flight must land before the pair ends
     if (!ok && rank == 0)
-      for (int i = it > a.stages ? it - a.stages : 0; i < it; i++)
+      for (int i = filled > a.stages ? filled - a.stages : 0; i < filled; i++)
         mbar_wait_bounded(&s.full[i % a.stages], (i / a.stages) & 1, a.err);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // -------------------------------------------------------- products
-    int it = 0, ti = 0;
+    Turn it;
+    int ti = 0;
     bool ok = true;
     for (int u = u0; u < units && ok; u += du, ti++) {
       const Tile t = tile_of(a, s, u, n_ct);
@@ -309,9 +327,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       ok = wait_or_stop(&s.acc_empty[ti & 1], ((ti >> 1) & 1) ^ 1, stop, a.err);
       if (!ok) break;
       tc_fence_after();
-      for (int kb = 0; kb < nkb; kb++, it++) {
-        const int st = it % a.stages;
-        ok = wait_or_stop(&s.full[st], (it / a.stages) & 1, stop, a.err);
+      for (int kb = 0; kb < nkb; kb++, it.next(a.stages)) {
+        const int st = it.st;
+        ok = wait_or_stop(&s.full[st], it.round, stop, a.err);
         if (!ok) break;
         tc_fence_after();
         const uint32_t A = smem_u32(ring + (size_t)st * a.stage_bytes);
