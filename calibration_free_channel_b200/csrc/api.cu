@@ -430,7 +430,7 @@ moe_status moe_reader_group_rows(int n, int n_groups, const int32_t* ids, int32_
 
 size_t moe_reader_grouped_workspace_bytes(int n_groups, int n_rows) {
   if (n_rows < 1 || n_rows > moe::kMaxRows || n_groups < 1 || n_groups > moe::kMaxGroups) return 0;
-  return kErrBytes;
+  return kErrBytes + moe::split_bytes(n_rows);
 }
 
 moe_status moe_reader_grouped_swiglu(int n_groups, int n_rows, int n_x, int I, int d, const uint16_t* x,
@@ -466,6 +466,7 @@ moe_status moe_reader_grouped_swiglu(int n_groups, int n_rows, int n_x, int I, i
   g.ldx = d;
   g.ldy = I;
   g.err = static_cast<uint32_t*>(workspace);
+  g.split = static_cast<char*>(workspace) + kErrBytes;
   cudaError_t e = moe::launch_grouped(g, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "grouped_swiglu launch");
 }
@@ -507,6 +508,7 @@ moe_status moe_reader_grouped_product(int n_groups, int n_rows, int n_x, int n_y
   g.ldy = N;
   g.y_rows = y_rows;
   g.err = static_cast<uint32_t*>(workspace);
+  g.split = static_cast<char*>(workspace) + kErrBytes;
   cudaError_t e = moe::launch_grouped(g, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "grouped_product launch");
 }
@@ -515,7 +517,7 @@ size_t moe_reader_adapter_workspace_bytes(int T, int n_adapters, int K, int N, i
   if (T < 1 || T > moe::kMaxRows || n_adapters < 1 || n_adapters > moe::kMaxGroups || K < 8 || N < 8 || r < 8 ||
       r > 128)
     return 0;
-  return kErrBytes;
+  return kErrBytes + moe::split_bytes(T) + sizeof(uint16_t) * 2 * moe::adapter_z_rows(T, n_adapters) * r;
 }
 
 moe_status moe_reader_adapter_product(int T, int n_adapters, int N, int K, int r, const uint16_t* x,
@@ -540,8 +542,10 @@ moe_status moe_reader_adapter_product(int T, int n_adapters, int N, int K, int r
   REQUIRE(x != y, "y must not be x");
   st = check_workspace(workspace, ws_bytes, moe_reader_adapter_workspace_bytes(T, n_adapters, K, N, r));
   if (st != MOE_OK) return st;
+  char* ws = static_cast<char*>(workspace);
   const moe::AdapterArgs g = {T, n_adapters, N, K, r, x, w, base, offsets, rows, a, b, scale, y,
-                              static_cast<uint32_t*>(workspace)};
+                              reinterpret_cast<uint32_t*>(ws), ws + kErrBytes,
+                              reinterpret_cast<uint16_t*>(ws + kErrBytes + moe::split_bytes(T))};
   cudaError_t e = moe::launch_adapter(g, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "adapter_product launch");
 }

@@ -114,7 +114,9 @@ size_t block_layout(int B, int E, int top_e, int I, int d, void* base, BlockArgs
     off = align256(off + bytes);
     return o;
   };
-  const size_t o_err = take(16), o_log = take(sizeof(double) * B * E), o_ids = take(sizeof(int32_t) * P),
+  // the error word and the split sums' counters sit where they do for every
+  // shape and every grouped entry point, so a workspace may be reused for another
+  const size_t o_err = take(16), o_split = take(split_bytes((int)P)), o_log = take(sizeof(double) * B * E), o_ids = take(sizeof(int32_t) * P),
                o_w = take(sizeof(float) * P), o_off = take(sizeof(int32_t) * (E + 1)),
                o_rows = take(sizeof(int32_t) * P), o_a = take(sizeof(uint16_t) * P * lda(I)),
                o_out = take(sizeof(float) * P * d);
@@ -128,6 +130,7 @@ size_t block_layout(int B, int E, int top_e, int I, int d, void* base, BlockArgs
     a->rows = reinterpret_cast<int32_t*>(p + o_rows);
     a->a = reinterpret_cast<uint16_t*>(p + o_a);
     a->out = reinterpret_cast<float*>(p + o_out);
+    a->split = p + o_split;
   }
   return off;
 }
@@ -157,6 +160,7 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
   g.ldx = a.d;
   g.ldy = lda(a.I);
   g.err = a.err;
+  g.split = a.split;
   e = launch_grouped(g, s);
   if (e != cudaSuccess) return e;
   GroupedArgs h = {};
@@ -177,6 +181,7 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
   h.y_fp32 = 1;
   h.y_rows = a.rows;
   h.err = a.err;
+  h.split = a.split;
   e = launch_grouped(h, s);
   if (e != cudaSuccess) return e;
   combine_kernel<<<a.B, 256, 0, s>>>(a);

@@ -21,7 +21,18 @@
 // For SwiGLU a CTA's 128 lanes are 64 gate and the same 64 up channels; the
 // warps of a gate and an up quarter swap half of their columns through shared
 // memory.
+//
+// Adapters: the tiles run over all tokens, sorted by adapter, and the shared
+// projection's sum over K goes on over the adapters that the tile meets, as
+// further stages: A is B_g, B the rows of z = scale x A_g^T (adapter.cu), the
+// accumulator's columns those of the adapter, widened to multiples of 32 with
+// zero rows.  So the low-rank term costs its own bytes and products only.
+//
+// A call with few tiles splits their sums over K: each part is written in
+// fp32, and the CTA that arrives last adds them in order and finishes the tile.
 #include <cudaTypedefs.h>
+
+#include <cstring>
 
 #include "kernels.h"
 #include "tensor.cuh"
@@ -56,11 +67,16 @@ constexpr int kBlockK = 64;                // K per stage: one 128-byte swizzled
 constexpr int kMaxCols = 256;              // rows per tile
 constexpr int kABytes = kLanes * kBlockK * 2;
 constexpr int kMaxStages = 8;
+constexpr int kMaxPairs = 74;              // CTA pairs of a launch
+constexpr int kMaxSplit = 8;               // parts of a tile's sum
 constexpr int kRowBoxes = 4;               // boxes of 128, 64, 32 and 16 rows
 constexpr int kSmemBudget = 227 * 1024 - 1024;  // 1024: the ring's alignment
 
+enum Mode { kPlain, kSwiglu, kAdapter };
+
 struct Maps {
   CUtensorMap x[kRowBoxes], w, w_up;
+  CUtensorMap z[kRowBoxes], b;  // adapters
 };
 
 struct TileArgs {
@@ -68,25 +84,31 @@ struct TileArgs {
   int cols;      // rows per tile at most (multiple of 32)
   int stages, stage_bytes;
   int layout, gather, x_div, y_fp32;
+  int max_split;
   const uint16_t* x;
   const int32_t* x_rows;
   const int32_t* offsets;
   const int32_t* y_rows;
   void* y;
   uint32_t* err;
+  uint32_t* count;        // [kMaxPairs][2] arrivals of a split tile's parts
+  float* part;            // [kMaxPairs][2][cols][128] the parts
+  // adapters (G of them; the tiles run over all P rows)
+  int r, has_w;
+  const uint16_t* base;
 };
 
 // Shared memory behind the ring.
 struct Side {
   uint64_t full[kMaxStages], landed[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
-  int stop, tiles;
+  int stop, tiles, last;
   int scan[kGThreads / 32];
   alignas(16) int y_row[kMaxCols];  // result row of each column, -1: none; even columns, then odd ones
   float swap[2][2][2][16][32];      // [quarter][turn][from the up side][column][lane]
   int first[kMaxGroups];            // first sorted position of each group
   int rows[kMaxGroups];             // rows of each group
-  int before[kMaxGroups + 1];       // row tiles of the groups before
+  int before[kMaxGroups + 1];       // row tiles of the groups before (adapters: rows of z before)
 };
 
 // A role's place in the ring: the stage, and how often it has gone round.
@@ -101,22 +123,23 @@ struct Turn {
 };
 
 // Checks the plan and lays its groups out as row tiles; every thread of the CTA.
+template <int kMode>
 __device__ void lay_tiles(const TileArgs& a, Side& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kPer = (kMaxGroups + kGThreads - 1) / kGThreads;
-  int n[kPer], t[kPer], sum = 0;
+  int t[kPer], sum = 0;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kPer; i++) {
     const int g = tid * kPer + i;
-    n[i] = t[i] = 0;
+    t[i] = 0;
     if (g < a.G) {
       const int p0 = a.offsets[g], p1 = a.offsets[g + 1];
-      bad |= p0 < 0 || p1 < p0 || p1 > a.P;
-      n[i] = p1 - p0;
-      t[i] = bad ? 0 : (n[i] + a.cols - 1) / a.cols;
+      const bool fine = p0 >= 0 && p1 >= p0 && p1 <= a.P;
+      bad |= !fine;
       s.first[g] = p0;
-      s.rows[g] = n[i];
+      s.rows[g] = fine ? p1 - p0 : 0;
+      if (fine) t[i] = kMode == kAdapter ? padded_rows(p0, p1) : (p1 - p0 + a.cols - 1) / a.cols;
     }
     sum += t[i];
   }
@@ -137,6 +160,7 @@ __device__ void lay_tiles(const TileArgs& a, Side& s) {
     run += t[i];
     if (g == a.G - 1) {
       s.before[a.G] = run;
+      if (kMode == kAdapter) run = (a.P + a.cols - 1) / a.cols;
       s.tiles = bad ? 0 : run;  // offsets that do not ascend within the rows: nothing is computed
       if (bad) atomicOr(a.err, kErrBadPlan);
     }
@@ -144,43 +168,108 @@ __device__ void lay_tiles(const TileArgs& a, Side& s) {
   __syncthreads();
 }
 
-struct Tile {
-  int g, p0, n, c0;  // group, first sorted position, rows, channel tile
+// The walk: units of work, each a tile and one of the parts of its sum.
+struct Walk {
+  int n_ct, split, units, nkb;  // channel tiles, parts per tile, units, stages of K
 };
-// Unit u of the walk: the channel tiles of a row tile follow one another (they
-// share its rows), the row tiles of a group too (they share its weights).
-__device__ __forceinline__ Tile tile_of(const TileArgs& a, const Side& s, int u, int n_ct) {
-  const int q = u / n_ct;
-  int lo = 0, hi = a.G - 1;  // the last group with before[g] <= q
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (s.before[m] <= q)
-      lo = m;
-    else
-      hi = m - 1;
+template <int kMode>
+__device__ __forceinline__ Walk walk_of(const TileArgs& a, const Side& s) {
+  constexpr int kChan = kMode == kSwiglu ? kLanes / 2 : kLanes;
+  Walk w;
+  w.n_ct = (a.N + 2 * kChan - 1) / (2 * kChan);
+  w.nkb = kMode == kAdapter && !a.has_w ? 0 : (a.K + kBlockK - 1) / kBlockK;
+  const int tiles = s.tiles * w.n_ct, pairs = gridDim.x >> 1;
+  w.split = 1;
+  if (tiles > 0 && 2 * tiles <= pairs) {
+    w.split = min(a.max_split, pairs / tiles);
+    if (w.nkb) w.split = min(w.split, max(1, w.nkb / 2));  // two stages each at least
+  }
+  w.units = tiles * w.split;
+  return w;
+}
+
+struct Tile {
+  int g, p0, n, c0;     // group, first sorted position, rows, channel tile
+  int index, part;      // of the tile, of its part
+  int k0, k1;           // stages of K
+};
+// Unit u: the parts of a tile follow one another, the channel tiles of a row
+// tile too (they share its rows), the row tiles of a group too (they share its
+// weights).
+template <int kMode>
+__device__ __forceinline__ Tile tile_of(const TileArgs& a, const Side& s, const Walk& w, int u) {
+  Tile t;
+  t.index = w.split == 1 ? u : u / w.split;
+  t.part = u - t.index * w.split;
+  t.k0 = w.nkb * t.part / w.split;
+  t.k1 = w.nkb * (t.part + 1) / w.split;
+  const int q = t.index / w.n_ct;
+  t.c0 = t.index - q * w.n_ct;
+  int lo = 0, rows = a.P, before = 0, first = 0;
+  if (kMode != kAdapter) {
+    int hi = a.G - 1;  // the last group with before[g] <= q
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (s.before[m] <= q)
+        lo = m;
+      else
+        hi = m - 1;
+    }
+    rows = s.rows[lo];
+    before = s.before[lo];
+    first = s.first[lo];
   }
   // a group's row tiles are as even as steps of 32 allow
-  const int rows = s.rows[lo], nt = (rows + a.cols - 1) / a.cols;
-  const int size = ((rows + nt - 1) / nt + 31) & ~31, at = (q - s.before[lo]) * size;
-  Tile t;
+  const int nt = (rows + a.cols - 1) / a.cols;
+  const int size = ((rows + nt - 1) / nt + 31) & ~31, at = (q - before) * size;
   t.g = lo;
-  t.p0 = s.first[lo] + at;
+  t.p0 = first + at;
   t.n = min(size, rows - at);
-  t.c0 = u - q * n_ct;
   return t;
+}
+
+// The stages that follow those of K: f(g, c, w, kb, h, nh) for adapter g with
+// columns [c, c + w) of the tile, block kb of its rank, and nh of z's two
+// halves from h (both where they fit into a stage).  Without a projection the
+// first is a stage of zeros (g = G) that sets the whole accumulator.  A split
+// tile's parts take them in turn.  f returns whether to go on.
+template <typename F>
+__device__ __forceinline__ bool adapter_steps(const TileArgs& a, const Side& s, const Walk& w, const Tile& t, F f) {
+  const int n = (t.n + 31) & ~31;
+  if (!a.has_w && !f(a.G, 0, n, 0, 0, 1)) return false;
+  int lo = 0, hi = a.G;  // the first adapter that ends behind p0
+  while (lo < hi) {
+    const int m = (lo + hi) >> 1;
+    if (s.first[m] + s.rows[m] > t.p0)
+      hi = m;
+    else
+      lo = m + 1;
+  }
+  int e = 0;
+  for (int g = lo; g < a.G && s.first[g] < t.p0 + t.n; g++) {
+    if (s.rows[g] == 0) continue;
+    const int c = max((s.first[g] & ~31) - t.p0, 0);
+    const int cols = min(((s.first[g] + s.rows[g] + 31) & ~31) - t.p0, n) - c;
+    const int nh = cols <= a.cols / 2 ? 2 : 1;
+    for (int kb = 0; kb * kBlockK < a.r; kb++)
+      for (int h = 0; h < 2; h += nh, e++)
+        if (e % w.split == t.part && !f(g, c, cols, kb, h, nh)) return false;
+  }
+  return true;
 }
 
 // The rows of x at sorted positions, gathered: thread i of 128 copies the
 // 16-byte piece i % 8 of rows i / 8 + 16 m of this CTA's half of the tile.  A
 // stage's copies arrive on landed[stage] as they complete; warp 3 passes that
 // on to the issuing CTA, so that the copying threads never wait for their copies.
-__device__ void gather_rows(const TileArgs& a, Side& s, uint8_t* ring, int units, int n_ct, int nkb, int rank) {
+template <int kMode>
+__device__ void gather_rows(const TileArgs& a, Side& s, uint8_t* ring, const Walk& w, int rank) {
   const int t = threadIdx.x - 256, piece = t & 7, r0 = t >> 3;
   volatile int* stop = &s.stop;
   Turn it;
   bool ok = true;
-  for (int u = blockIdx.x >> 1; u < units && ok; u += gridDim.x >> 1) {
-    const Tile tl = tile_of(a, s, u, n_ct);
+  for (int u = blockIdx.x >> 1; u < w.units && ok; u += gridDim.x >> 1) {
+    const Tile tl = tile_of<kMode>(a, s, w, u);
     const int half = ((tl.n + 31) & ~31) >> 1;
     const uint16_t* src[8];
 #pragma unroll
@@ -197,45 +286,63 @@ __device__ void gather_rows(const TileArgs& a, Side& s, uint8_t* ring, int units
       }
       src[m] = a.x + (size_t)row * a.ldx + piece * 8;
     }
-    for (int kb = 0; kb < nkb; kb++, it.next(a.stages)) {
-      const int st = it.st;
-      ok = wait_or_stop(&s.empty[st], it.round ^ 1, stop, a.err);
-      if (__any_sync(0xffffffffu, !ok)) {
-        ok = false;
-        break;
-      }
-      const uint32_t dst = smem_u32(ring + (size_t)st * a.stage_bytes + kABytes) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
+    auto stage_free = [&] {
+      ok = wait_or_stop(&s.empty[it.st], it.round ^ 1, stop, a.err);
+      ok = !__any_sync(0xffffffffu, !ok);
+      return ok;
+    };
+    for (int kb = tl.k0; kb < tl.k1; kb++, it.next(a.stages)) {
+      if (!stage_free()) break;
+      const uint32_t dst =
+          smem_u32(ring + (size_t)it.st * a.stage_bytes + kABytes) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
       const bool in = kb * kBlockK + piece * 8 < a.K;
 #pragma unroll
       for (int m = 0; m < 8; m++)
         if (r0 + 16 * m < half) cp_async16(dst + m * 2048, in ? src[m] + kb * kBlockK : a.x, in);
-      cp_async_arrive(&s.landed[st]);
+      cp_async_arrive(&s.landed[it.st]);
     }
+    if (kMode == kAdapter && ok)  // nothing to copy, but the stage is announced like any other
+      adapter_steps(a, s, w, tl, [&](int, int, int, int, int, int) {
+        if (!stage_free()) return false;
+        cp_async_arrive(&s.landed[it.st]);
+        it.next(a.stages);
+        return true;
+      });
   }
   cp_async_wait_all();
 }
 
 // Passes each stage of gathered rows on: complete here, made visible to the
 // tensor cores, announced to the issuing CTA.
-__device__ void announce_rows(const TileArgs& a, Side& s, int units, int nkb) {
+template <int kMode>
+__device__ void announce_rows(const TileArgs& a, Side& s, const Walk& w) {
   const uint32_t full = peer_u32(s.full, 0);
   Turn it;
-  for (int u = blockIdx.x >> 1; u < units; u += gridDim.x >> 1)
-    for (int kb = 0; kb < nkb; kb++, it.next(a.stages)) {
-      if (!wait_or_stop(&s.landed[it.st], it.round, &s.stop, a.err)) return;
-      fence_proxy_async();
-      mbar_arrive_at(full + it.st * 8);
-    }
+  auto pass_on = [&] {
+    if (!wait_or_stop(&s.landed[it.st], it.round, &s.stop, a.err)) return false;
+    fence_proxy_async();
+    mbar_arrive_at(full + it.st * 8);
+    it.next(a.stages);
+    return true;
+  };
+  for (int u = blockIdx.x >> 1; u < w.units; u += gridDim.x >> 1) {
+    const Tile t = tile_of<kMode>(a, s, w, u);
+    for (int kb = t.k0; kb < t.k1; kb++)
+      if (!pass_on()) return;
+    if (kMode == kAdapter &&
+        !adapter_steps(a, s, w, t, [&](int, int, int, int, int, int) { return pass_on(); }))
+      return;
+  }
 }
 
-template <bool kSwiglu>
+template <int kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     tiles_kernel(const __grid_constant__ Maps maps, const TileArgs a) {
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   Side& s = *reinterpret_cast<Side*>(ring + (size_t)a.stages * a.stage_bytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x & 1;
-  constexpr int kChan = kSwiglu ? kLanes / 2 : kLanes;  // output channels per CTA
+  constexpr int kChan = kMode == kSwiglu ? kLanes / 2 : kLanes;  // output channels per CTA
   if (tid == 0) {
     for (int i = 0; i < a.stages; i++) {
       mbar_init(&s.full[i], a.gather ? 3 : 1);  // the boxes' announcement, and the gathered rows' of each CTA
@@ -249,67 +356,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     mbar_init(&s.drain, 1);
     s.stop = 0;
     fence_mbar_init();
-    for (int i = 0; i < kRowBoxes; i++) tma_prefetch(&maps.x[i]);
+    for (int i = 0; i < kRowBoxes; i++) tma_prefetch(kMode == kAdapter ? &maps.z[i] : &maps.x[i]);
     tma_prefetch(&maps.w);
-    if (kSwiglu) tma_prefetch(&maps.w_up);
+    if (kMode == kSwiglu) tma_prefetch(&maps.w_up);
+    if (kMode == kAdapter) tma_prefetch(&maps.b);
   }
   if (warp == 2) tmem_alloc(&s.tmem, 512);
-  pdl_trigger();
-  pdl_wait();
+  // Adapters: the launch before this one (adapter.cu) lets it start only once
+  // everything earlier has completed, so only z, which it writes, is waited for.
+  if (kMode != kAdapter) {
+    pdl_trigger();
+    pdl_wait();
+  }
   tc_fence_before();
-  lay_tiles(a, s);
+  lay_tiles<kMode>(a, s);
   cluster_arrive();
   cluster_wait();  // the pair's barriers are ready
   tc_fence_after();
   const uint32_t tmem = s.tmem;
-  const int n_ct = (a.N + 2 * kChan - 1) / (2 * kChan), units = s.tiles * n_ct, nkb = (a.K + kBlockK - 1) / kBlockK;
+  const Walk w = walk_of<kMode>(a, s);
   const int u0 = blockIdx.x >> 1, du = gridDim.x >> 1;
   volatile int* stop = &s.stop;
 
-  if ((warp == 0 || (warp == 2 && !a.gather)) && lane == 0) {
+  if ((warp == 0 || (warp == 2 && (!a.gather || kMode == kAdapter))) && lane == 0) {
     // ----------------------- boxes: the weights (warp 0), the rows (warp 2)
     const bool rows = warp == 2;
     Turn it;
     int filled = 0;
     bool ok = true;
     const uint32_t full = peer_u32(s.full, 0);
-    for (int u = u0; u < units && ok; u += du) {
-      const Tile t = tile_of(a, s, u, n_ct);
+    // `half` rows from row p of a matrix, in boxes of 128, 64, 32 and 16
+    auto fetch_rows = [&](uint8_t* B, const CUtensorMap* m, int half, auto copy) {
+      if (half == 128) {
+        copy(B, &m[0], 0);
+        return;
+      }
+      int at = 0;
+#pragma unroll
+      for (int b = 1; b < kRowBoxes; b++)
+        if (half & (128 >> b)) {
+          copy(B + at * 128, &m[b], at);
+          at += 128 >> b;
+        }
+    };
+    if (kMode == kAdapter && rows) pdl_wait();
+    for (int u = u0; u < w.units && ok; u += du) {
+      const Tile t = tile_of<kMode>(a, s, w, u);
       const int half = ((t.n + 31) & ~31) >> 1, c0 = (t.c0 * 2 + rank) * kChan, p = t.p0 + rank * half;
       const uint32_t bytes = 2 * (kABytes + (a.gather ? 0 : half * 128));  // of both CTAs
-      for (int k0 = 0; k0 < a.K; k0 += kBlockK, it.next(a.stages), filled++) {
+      for (int kb = t.k0; kb < t.k1; kb++, it.next(a.stages), filled++) {
+        const int k0 = kb * kBlockK;
+        if (kMode == kAdapter && rows) continue;  // gathered
         ok = wait_or_stop(&s.empty[it.st], it.round ^ 1, stop, a.err);
         if (!ok) break;
         uint8_t* A = ring + (size_t)it.st * a.stage_bytes;
         const uint32_t bar = full + it.st * 8;
         if (rows) {
-          uint8_t* B = A + kABytes;
-          if (half == 128) {
-            tma_2d(B, &maps.x[0], k0, p, bar);
-          } else {
-            int at = 0;
-#pragma unroll
-            for (int b = 1; b < kRowBoxes; b++) {
-              const int h = 128 >> b;
-              if (half & h) {
-                tma_2d(B + at * 128, &maps.x[b], k0, p + at, bar);
-                at += h;
-              }
-            }
-          }
+          fetch_rows(A + kABytes, maps.x, half,
+                     [&](uint8_t* to, const CUtensorMap* m, int at) { tma_2d(to, m, k0, p + at, bar); });
           continue;
         }
         if (rank == 0) mbar_expect_tx(&s.full[it.st], bytes);
-        if (kSwiglu) {
+        if (kMode == kSwiglu) {
           tma_3d(A, &maps.w, k0, c0, t.g, bar);
           tma_3d(A + kABytes / 2, &maps.w_up, k0, c0, t.g, bar);
-        } else if (a.layout) {
+        } else if (kMode == kPlain && a.layout) {
           tma_3d(A, &maps.w, c0, k0, t.g, bar);
           tma_3d(A + kABytes / 2, &maps.w, c0 + 64, k0, t.g, bar);
         } else {
           tma_3d(A, &maps.w, k0, c0, t.g, bar);
         }
       }
+      if (kMode == kAdapter && ok)
+        ok = adapter_steps(a, s, w, t, [&](int g, int c, int cols, int kb, int h, int nh) {
+          if (!wait_or_stop(&s.empty[it.st], it.round ^ 1, stop, a.err)) return false;
+          uint8_t* A = ring + (size_t)it.st * a.stage_bytes;
+          const uint32_t bar = full + it.st * 8;
+          if (rows) {
+            // rows of z: those of the column range, this CTA's half of them
+            const int hc = cols >> 1;
+            const int zr = g < a.G ? s.before[g] + t.p0 + c - (s.first[g] & ~31) + rank * hc : 0;
+            for (int i = 0; i < nh; i++)
+              fetch_rows(A + kABytes + i * hc * 128, maps.z, hc, [&](uint8_t* to, const CUtensorMap* m, int at) {
+                tma_3d(to, m, kb * kBlockK, zr + at, g < a.G ? h + i : 2, bar);  // 2: outside, zeros
+              });
+          } else {
+            if (rank == 0) mbar_expect_tx(&s.full[it.st], 2 * (kABytes + nh * (cols >> 1) * 128));
+            tma_3d(A, &maps.b, kb * kBlockK, c0, g, bar);  // adapter G: outside, zeros
+          }
+          it.next(a.stages);
+          filled++;
+          return true;
+        });
     }
     // after a timeout: the copies in flight must land before the pair ends
     if (!ok && rank == 0)
@@ -320,30 +458,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     Turn it;
     int ti = 0;
     bool ok = true;
-    for (int u = u0; u < units && ok; u += du, ti++) {
-      const Tile t = tile_of(a, s, u, n_ct);
+    for (int u = u0; u < w.units && ok; u += du, ti++) {
+      const Tile t = tile_of<kMode>(a, s, w, u);
       const uint32_t d = tmem + (ti & 1) * kMaxCols;
-      const uint32_t idesc = mma_desc(2 * kLanes, (t.n + 31) & ~31, !kSwiglu && a.layout);
+      const bool mn_a = kMode == kPlain && a.layout;
+      const uint32_t idesc = mma_desc(2 * kLanes, (t.n + 31) & ~31, mn_a);
       ok = wait_or_stop(&s.acc_empty[ti & 1], ((ti >> 1) & 1) ^ 1, stop, a.err);
       if (!ok) break;
       tc_fence_after();
-      for (int kb = 0; kb < nkb; kb++, it.next(a.stages)) {
-        const int st = it.st;
-        ok = wait_or_stop(&s.full[st], it.round, stop, a.err);
+      for (int kb = t.k0; kb < t.k1; kb++, it.next(a.stages)) {
+        ok = wait_or_stop(&s.full[it.st], it.round, stop, a.err);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t A = smem_u32(ring + (size_t)st * a.stage_bytes);
+        const uint32_t A = smem_u32(ring + (size_t)it.st * a.stage_bytes);
         const uint64_t bd = tile_desc(A + kABytes, 16);
         const int steps = (min(kBlockK, a.K - kb * kBlockK) + 15) / 16;  // past K the stage holds zeros
-        if (!kSwiglu && a.layout) {
+        if (mn_a) {
           const uint64_t ad = tile_desc(A, kABytes / 2);
-          for (int k = 0; k < steps; k++) mma_bf16(d, ad + k * (2048 >> 4), bd + k * 2, idesc, kb + k > 0);
+          for (int k = 0; k < steps; k++) mma_bf16(d, ad + k * (2048 >> 4), bd + k * 2, idesc, kb + k > t.k0);
         } else {
           const uint64_t ad = tile_desc(A, 16);
-          for (int k = 0; k < steps; k++) mma_bf16(d, ad + k * 2, bd + k * 2, idesc, kb + k > 0);
+          for (int k = 0; k < steps; k++) mma_bf16(d, ad + k * 2, bd + k * 2, idesc, kb + k > t.k0);
         }
-        mma_commit(&s.empty[st]);
+        mma_commit(&s.empty[it.st]);
       }
+      if (kMode == kAdapter && ok)
+        ok = adapter_steps(a, s, w, t, [&](int g, int c, int cols, int kb, int h, int nh) {
+          if (!wait_or_stop(&s.full[it.st], it.round, stop, a.err)) return false;
+          tc_fence_after();
+          const uint32_t A = smem_u32(ring + (size_t)it.st * a.stage_bytes);
+          const uint64_t ad = tile_desc(A, 16);
+          const uint32_t id = mma_desc(2 * kLanes, cols, false);
+          const int steps = g < a.G ? (min(kBlockK, a.r - kb * kBlockK) + 15) / 16 : 1;
+          for (int i = 0; i < nh; i++) {
+            const uint64_t bd = tile_desc(A + kABytes + i * (cols >> 1) * 128, 16);
+            for (int k = 0; k < steps; k++) mma_bf16(d + c, ad + k * 2, bd + k * 2, id, g < a.G);
+          }
+          mma_commit(&s.empty[it.st]);
+          it.next(a.stages);
+          return true;
+        });
       if (ok) mma_commit(&s.acc_full[ti & 1]);
     }
     if (!ok) {  // after a timeout: the products in flight must end before the pair does
@@ -351,16 +505,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       mbar_wait_bounded(&s.drain, 0, a.err);
     }
   } else if (warp == 3 && lane == 0) {
-    if (a.gather) announce_rows(a, s, units, nkb);
+    if (a.gather) announce_rows<kMode>(a, s, w);
   } else if (warp >= 8) {
-    if (a.gather) gather_rows(a, s, ring, units, n_ct, nkb, rank);
+    if (a.gather) gather_rows<kMode>(a, s, ring, w, rank);
   } else if (warp >= 4) {
     // ------------------------------------------------- read back, store
     const int q4 = warp - 4, et = tid - 128;
     const bool odd = lane & 1;
     int ti = 0, turn = 0;
-    for (int u = u0; u < units; u += du, ti++) {
-      const Tile t = tile_of(a, s, u, n_ct);
+    for (int u = u0; u < w.units; u += du, ti++) {
+      const Tile t = tile_of<kMode>(a, s, w, u);
       for (int j = et; j < ((t.n + 31) & ~31); j += 128) {
         int q = -1;
         if (j < t.n) {
@@ -380,10 +534,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       if (bar_any(1, 128, !ok)) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q4 * 32) << 16) + (ti & 1) * kMaxCols;
-      for (int j0 = 0; j0 < t.n; j0 += 32) {
+      bool finish = true;
+      const size_t part_size = (size_t)2 * a.cols * kLanes;
+      float* part0 = a.part + (size_t)t.index * w.split * part_size + (size_t)rank * a.cols * kLanes + q4 * 32 + lane;
+      if (w.split > 1) {
+        float* mine = part0 + t.part * part_size;
+        for (int j0 = 0; j0 < t.n; j0 += 32) {
+          float v[32];
+          tmem_ld32(acc + j0, v);
+#pragma unroll
+          for (int j = 0; j < 32; j++) __stcg(mine + (j0 + j) * kLanes, v[j]);
+        }
+        __threadfence();
+        bar_any(1, 128, false);
+        if (et == 0) {
+          uint32_t* count = a.count + t.index * 2 + rank;
+          const bool last = atomicAdd(count, 1u) == (uint32_t)w.split - 1;
+          if (last) *count = 0u;  // as it was found
+          __threadfence();
+          s.last = last;
+        }
+        bar_any(1, 128, false);
+        finish = s.last != 0;
+      }
+      for (int j0 = 0; j0 < t.n && finish; j0 += 32) {
         float v[32];
-        tmem_ld32(acc + j0, v);
-        if (kSwiglu) {
+        if (w.split > 1) {
+#pragma unroll
+          for (int j = 0; j < 32; j++) v[j] = 0.0f;
+          for (int i = 0; i < w.split; i++) {
+            const float* p = part0 + i * part_size + j0 * kLanes;
+#pragma unroll
+            for (int j = 0; j < 32; j++) v[j] += __ldcg(p + j * kLanes);
+          }
+        } else {
+          tmem_ld32(acc + j0, v);
+        }
+        if (kMode == kSwiglu) {
           // the gate side finishes the even columns, the up side the odd ones
           const bool up = q4 >= 2;
           float(&out)[16][32] = s.swap[q4 & 1][turn][up ? 1 : 0];
@@ -395,8 +582,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           float r[16];
 #pragma unroll
           for (int i = 0; i < 16; i++) {
-            const float o = in[i][lane], g = up ? o : v[2 * i], w = up ? v[2 * i + 1] : o;
-            r[i] = __fdividef(g, 1.0f + __expf(-g)) * w;
+            const float o = in[i][lane], g = up ? o : v[2 * i], m = up ? v[2 * i + 1] : o;
+            r[i] = __fdividef(g, 1.0f + __expf(-g)) * m;
           }
           const int* q_of = s.y_row + (up ? kMaxCols / 2 : 0) + (j0 >> 1);
           const int cw = (t.c0 * 2 + rank) * kChan + (q4 & 1) * 32;
@@ -410,17 +597,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             }
           } else {
             const int c = cw + (lane & ~1);
-            if (c < a.N) y += c;
             const bool in_n = c < a.N;
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               const float o = __shfl_xor_sync(0xffffffffu, odd ? r[i] : r[i + 1], 1);
-              const uint32_t w = odd ? bf16x2(o, r[i + 1]) : bf16x2(r[i], o);
+              const uint32_t p2 = odd ? bf16x2(o, r[i + 1]) : bf16x2(r[i], o);
               const int q = q_of[i + (odd ? 1 : 0)];
-              if (q >= 0 && in_n) *reinterpret_cast<uint32_t*>(y + (size_t)q * a.ldy) = w;
+              if (q >= 0 && in_n) *reinterpret_cast<uint32_t*>(y + (size_t)q * a.ldy + c) = p2;
             }
           }
-        } else if (a.y_fp32) {
+        } else if (kMode == kPlain && a.y_fp32) {
           const int c = (t.c0 * 2 + rank) * kChan + q4 * 32 + lane;
           const bool in_n = c < a.N;
           float* y = static_cast<float*>(a.y) + c;
@@ -434,18 +620,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           const int c = (t.c0 * 2 + rank) * kChan + q4 * 32 + (lane & ~1);
           const bool in_n = c < a.N;
           uint16_t* y = static_cast<uint16_t*>(a.y) + c;
+          int qs[16];
           const int4* q_of = reinterpret_cast<const int4*>(s.y_row + (odd ? kMaxCols / 2 : 0) + (j0 >> 1));
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const int4 q = q_of[i];
-            const int qs[4] = {q.x, q.y, q.z, q.w};
+          for (int i = 0; i < 4; i++) *reinterpret_cast<int4*>(qs + 4 * i) = q_of[i];
+          uint32_t bw[16];
+          if (kMode == kAdapter && a.base) {
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-              const int j = 8 * i + 2 * k;
-              const float o = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-              const uint32_t w = odd ? bf16x2(o, v[j + 1]) : bf16x2(v[j], o);
-              if (qs[k] >= 0 && in_n) *reinterpret_cast<uint32_t*>(y + (size_t)qs[k] * a.ldy) = w;
+            for (int i = 0; i < 16; i++)
+              bw[i] = qs[i] >= 0 && in_n ? *reinterpret_cast<const uint32_t*>(a.base + (size_t)qs[i] * a.ldy + c) : 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            const float o = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+            float lo = odd ? o : v[2 * i], hi = odd ? v[2 * i + 1] : o;
+            if (kMode == kAdapter && a.base) {
+              lo += bf16lo(bw[i]);
+              hi += bf16hi(bw[i]);
             }
+            if (qs[i] >= 0 && in_n) *reinterpret_cast<uint32_t*>(y + (size_t)qs[i] * a.ldy) = bf16x2(lo, hi);
           }
         }
       }
@@ -460,45 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   cluster_arrive();
   cluster_wait();  // neither CTA leaves while the other may still signal it
   if (warp == 2) tmem_free(tmem, 512);
-}
-
-// One CTA per (token position, 256 channels).
-__global__ void __launch_bounds__(256) adapter_kernel(AdapterArgs a) {
-  extern __shared__ float sh[];
-  float* xs = sh;        // [K]
-  float* z = sh + a.K;   // [r]
-  const int p = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t = a.rows[p];
-  if (t < 0 || t >= a.T) {
-    if (tid == 0) atomicOr(a.err, kErrBadPlan);
-    return;
-  }
-  int lo = 0, hi = a.A;  // the first group that ends behind p
-  while (lo < hi) {
-    const int m = (lo + hi) >> 1;
-    if (a.offsets[m + 1] > p) hi = m; else lo = m + 1;
-  }
-  const int g = lo;
-  for (int k = tid; k < a.K; k += 256) xs[k] = bf16f(a.x[(size_t)t * a.K + k]);
-  __syncthreads();
-  for (int j = warp; j < a.r; j += 8) {
-    float s = 0.0f;
-    if (g < a.A) {
-      for (int k = lane; k < a.K; k += 32) s = fmaf(xs[k], bf16f(a.a[((size_t)g * a.r + j) * a.K + k]), s);
-      s = warp_sum(s) * (a.scale ? a.scale[g] : 1.0f);
-    }
-    if (lane == 0) z[j] = s;
-  }
-  __syncthreads();
-  const int n = blockIdx.y * 256 + tid;
-  if (n >= a.N) return;
-  float s = 0.0f;
-  if (a.w)
-    for (int k = 0; k < a.K; k++) s = fmaf(xs[k], bf16f(a.w[(size_t)n * a.K + k]), s);
-  if (g < a.A)
-    for (int j = 0; j < a.r; j++) s = fmaf(z[j], bf16f(a.b[((size_t)g * a.N + n) * a.r + j]), s);
-  if (a.base) s += bf16f(a.base[(size_t)t * a.N + n]);
-  a.y[(size_t)t * a.N + n] = f2bf16(s);
+  if (kMode == kAdapter) pdl_wait();  // whoever waits for this launch waits for the one before it too
 }
 
 int sm_count() {
@@ -512,20 +667,31 @@ int sm_count() {
   return count;
 }
 
-template <bool kSwiglu>
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Rows per tile at most for n rows: all of them up to 256.
+int most_cols(int n) { return n < kMaxCols ? (n + 31) / 32 * 32 : kMaxCols; }
+
+template <int kMode>
 cudaError_t run_tiles(const Maps& m, TileArgs t, cudaStream_t s) {
   t.stage_bytes = kABytes + t.cols / 2 * 128;
   t.stages = (kSmemBudget - (int)sizeof(Side)) / t.stage_bytes;
   if (t.stages > kMaxStages) t.stages = kMaxStages;
+  t.max_split = kMaxSplit;
   const size_t smem = 1024 + (size_t)t.stages * t.stage_bytes + sizeof(Side);
-  cudaError_t e = cudaFuncSetAttribute(tiles_kernel<kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(tiles_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const int chan = kSwiglu ? kLanes : 2 * kLanes, n_ct = (t.N + chan - 1) / chan;
-  const long most = ((long)(t.P + t.cols - 1) / t.cols + (t.G < t.P ? t.G : t.P)) * n_ct;  // units at most
+  if (sms < 2) return cudaErrorInvalidDevice;
+  const int pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
+  const int chan = kMode == kSwiglu ? kLanes : 2 * kLanes;
+  const long n_ct = (t.N + chan - 1) / chan;
+  // units at most: the tiles, each in as many parts as there may be
+  long most = (long)(t.P + t.cols - 1) / t.cols;
+  if (kMode != kAdapter) most += t.G < t.P ? t.G : t.P;
+  most *= n_ct * kMaxSplit;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * (most < sms / 2 ? most : sms / 2)));
+  cfg.gridDim = dim3((unsigned)(2 * (most < pairs ? most : pairs)));
   cfg.blockDim = dim3(kGThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -534,10 +700,35 @@ cudaError_t run_tiles(const Maps& m, TileArgs t, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tiles_kernel<kSwiglu>, m, t);
+  return cudaLaunchKernelEx(&cfg, tiles_kernel<kMode>, m, t);
+}
+
+// Rows per tile: the most, halved while a call's tiles would leave more than
+// half of the CTA pairs without one (the weights are then read once per row
+// tile, from L2).
+int choose_cols(int n, int groups, int N, int chan) {
+  int cols = most_cols(n);
+  const long n_ct = (N + chan - 1) / chan;
+  while (cols > 32) {
+    const long row_tiles = (n + cols - 1) / cols;
+    if ((row_tiles > groups ? row_tiles : groups) * n_ct * 2 > kMaxPairs) break;
+    cols = (cols / 2 + 31) / 32 * 32;
+  }
+  return cols;
+}
+
+bool row_maps(CUtensorMap* m, const void* base, uint64_t x, uint64_t y, uint64_t z, uint64_t row_bytes,
+              uint64_t mat_bytes) {
+  for (int b = 0; b < kRowBoxes; b++)
+    if (!tensor_map(&m[b], base, x, y, z, row_bytes, mat_bytes, kBlockK, 128 >> b)) return false;
+  return true;
 }
 
 }  // namespace
+
+size_t split_bytes(int n_rows) {
+  return align256(sizeof(uint32_t) * 2 * kMaxPairs) + sizeof(float) * 2 * kMaxPairs * kLanes * (size_t)most_cols(n_rows);
+}
 
 cudaError_t launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   TileArgs t = {};
@@ -547,42 +738,65 @@ cudaError_t launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   t.n_y = a.n_y;
   t.N = a.N;
   t.K = a.K;
+  t.ldx = a.ldx;
   t.ldy = a.ldy;
   t.layout = a.layout;
   t.gather = a.x_rows != nullptr;
   t.x_div = a.x_div;
   t.y_fp32 = a.y_fp32;
+  t.x = a.x;
   t.x_rows = a.x_rows;
   t.offsets = a.offsets;
   t.y_rows = a.y_rows;
   t.y = a.y;
   t.err = a.err;
-  t.cols = a.P < kMaxCols ? (a.P + 31) / 32 * 32 : kMaxCols;
-  t.x = a.x;
-  t.ldx = a.ldx;
+  t.count = static_cast<uint32_t*>(a.split);
+  t.part = reinterpret_cast<float*>(static_cast<char*>(a.split) + align256(sizeof(uint32_t) * 2 * kMaxPairs));
+  t.cols = choose_cols(a.P, a.G < a.P ? a.G : a.P, a.N, a.w_up ? kLanes : 2 * kLanes);
   Maps m;
+  memset(&m, 0, sizeof m);
   const uint64_t N = a.N, K = a.K;
-  bool ok = true;
-  for (int b = 0; b < kRowBoxes; b++)
-    ok = ok && tensor_map(&m.x[b], a.x, K, a.n_x, 0, 2ull * a.ldx, 0, kBlockK, 128 >> b);
-  if (a.w_up) {
+  bool ok = row_maps(m.x, a.x, K, a.n_x, 0, 2ull * a.ldx, 0);
+  if (a.w_up)
     ok = ok && tensor_map(&m.w, a.w, K, N, a.G, 2 * K, 2 * N * K, kBlockK, kLanes / 2) &&
          tensor_map(&m.w_up, a.w_up, K, N, a.G, 2 * K, 2 * N * K, kBlockK, kLanes / 2);
-  } else {
+  else
     ok = ok && (a.layout ? tensor_map(&m.w, a.w, N, K, a.G, 2 * N, 2 * N * K, 64, kBlockK)
                          : tensor_map(&m.w, a.w, K, N, a.G, 2 * K, 2 * N * K, kBlockK, kLanes));
-    m.w_up = m.w;
-  }
   if (!ok) return cudaErrorInvalidValue;
-  return a.w_up ? run_tiles<true>(m, t, s) : run_tiles<false>(m, t, s);
+  return a.w_up ? run_tiles<kSwiglu>(m, t, s) : run_tiles<kPlain>(m, t, s);
 }
 
 cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s) {
-  const size_t smem = sizeof(float) * (a.K + a.r);
-  cudaError_t e = cudaFuncSetAttribute(adapter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = launch_adapter_down(a, s);
   if (e != cudaSuccess) return e;
-  adapter_kernel<<<dim3(a.T, (a.N + 255) / 256), 256, smem, s>>>(a);
-  return cudaGetLastError();
+  TileArgs t = {};
+  t.G = a.A;
+  t.P = t.n_x = t.n_y = a.T;
+  t.N = t.ldy = a.N;
+  t.K = t.ldx = a.K;
+  t.gather = 1;
+  t.x_div = 1;
+  t.x = a.x;
+  t.x_rows = t.y_rows = a.rows;
+  t.offsets = a.offsets;
+  t.y = a.y;
+  t.err = a.err;
+  t.count = static_cast<uint32_t*>(a.split);
+  t.part = reinterpret_cast<float*>(static_cast<char*>(a.split) + align256(sizeof(uint32_t) * 2 * kMaxPairs));
+  t.r = a.r;
+  t.has_w = a.w != nullptr;
+  t.base = a.base;
+  t.cols = choose_cols(a.T, 1, a.N, 2 * kLanes);
+  Maps m;
+  memset(&m, 0, sizeof m);
+  const uint64_t N = a.N, K = a.K, r = a.r, zr = adapter_z_rows(a.T, a.A);
+  const bool ok = row_maps(m.z, a.z, r, zr, 2, 2 * r, 2 * r * zr) &&
+                  tensor_map(&m.b, a.b, r, N, a.A, 2 * r, 2 * r * N, kBlockK, kLanes) &&
+                  (!a.w || tensor_map(&m.w, a.w, K, N, 1, 2 * K, 2 * N * K, kBlockK, kLanes));
+  if (!ok) return cudaErrorInvalidValue;
+  if (!a.w) m.w = m.b;
+  return run_tiles<kAdapter>(m, t, s);
 }
 
 }  // namespace moe

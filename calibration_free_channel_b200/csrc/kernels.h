@@ -172,7 +172,10 @@ struct GroupedArgs {
   int y_fp32;
   const int32_t* y_rows;    // [P] or null
   uint32_t* err;
+  void* split;              // split_bytes(P) of workspace, zero before first use
 };
+// What tiles whose sum is split over CTAs meet in: counters and fp32 parts.
+size_t split_bytes(int n_rows);
 cudaError_t launch_grouped(const GroupedArgs& a, cudaStream_t s);
 
 struct AdapterArgs {
@@ -187,8 +190,15 @@ struct AdapterArgs {
   const float* scale;
   uint16_t* y;
   uint32_t* err;
+  void* split;        // split_bytes(T)
+  uint16_t* z;        // [2, adapter_z_rows(T, A), r]: scale x A^T, its bf16 value and what that leaves
 };
 cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s);
+// z (adapter.cu), before the tiles that read it.
+cudaError_t launch_adapter_down(const AdapterArgs& a, cudaStream_t s);
+// Rows of z: an adapter's sorted positions, widened to multiples of 32.
+__host__ __device__ inline int padded_rows(int p0, int p1) { return p1 > p0 ? ((p1 + 31) & ~31) - (p0 & ~31) : 0; }
+inline size_t adapter_z_rows(int T, int A) { return (size_t)T + 64 * (size_t)(A < T ? A : T); }
 
 struct BlockArgs {
   int B, E, I, d, top_e;
@@ -210,6 +220,7 @@ struct BlockArgs {
   int32_t* rows;      // [B * top_e]
   uint16_t* a;        // [B * top_e, I rounded up to 8]
   float* out;         // [B * top_e, d]
+  void* split;        // split_bytes(B * top_e)
 };
 size_t block_layout(int B, int E, int top_e, int I, int d, void* base, BlockArgs* a);
 cudaError_t launch_block(const BlockArgs& a, cudaStream_t s);

@@ -333,7 +333,9 @@ moe_status moe_reader_forward_noalloc(const moe_reader_layer* layer, int B, int 
  *    call's are.
  *  - The workspace rules of moe_reader_forward hold (zero-filled once before
  *    first use, not shared by calls that may overlap; two captured graphs
- *    that may run at the same time need two workspaces).  Calls may be
+ *    that may run at the same time need two workspaces).  One workspace
+ *    serves all of these entry points in turn, at any sizes that it is large
+ *    enough for; zero-fill it again after MOE_ETIMEOUT.  Calls may be
  *    captured into a graph and replayed.
  * ------------------------------------------------------------------------ */
 
