@@ -423,8 +423,7 @@ moe_status moe_reader_group_rows(int n, int n_groups, const int32_t* ids, int32_
   REQUIRE_PTR(rows);
   st = check_workspace(workspace, ws_bytes, moe_reader_group_workspace_bytes(n, n_groups));
   if (st != MOE_OK) return st;
-  cudaError_t e = moe::launch_group_rows(n, n_groups, ids, offsets, rows, static_cast<uint32_t*>(workspace),
-                                         static_cast<cudaStream_t>(stream));
+  cudaError_t e = moe::launch_group_rows(n, n_groups, ids, offsets, rows, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "group_rows launch");
 }
 

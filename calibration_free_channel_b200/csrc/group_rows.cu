@@ -1,5 +1,15 @@
-// group_rows.cu -- the plan of a grouped product: row numbers sorted by
-// group id, stable, with the groups' offsets (a counting sort).
+// group_rows.cu -- the plan of a grouped product: row numbers sorted by group
+// id, stable, with the groups' offsets.
+//
+// A counting sort in one launch.  Every warp owns a stretch of the ids and
+// counts them by group in a table of its own (32 ids at a time: lanes with
+// equal ids find each other and one adds for all), the warps' and CTAs' counts
+// are summed in order, and every warp walks its stretch again and places its
+// rows.  No atomics, so the order is that of the rows.
+//
+// The work is a few bytes a row; what bounds it is the chain of dependent
+// steps.  Up to 4096 rows one CTA does all (no cluster to wait for), above
+// that a cluster of eight, whose counts meet in distributed shared memory.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -7,65 +17,142 @@ namespace moe {
 
 namespace {
 
-// One CTA: histogram, exclusive scan, then the rows chunk by chunk, the warps
-// of a chunk in turn, so that rows of one group keep their order.
-__global__ void __launch_bounds__(1024) group_rows_kernel(int n, int G, const int32_t* __restrict__ ids,
+constexpr int kSortWarps = 32;
+constexpr int kBatch = 8;  // ids a lane loads at a time
+
+struct SortSide {
+  int total[kMaxGroups + 1];  // this CTA's rows of each group, then the first position of each
+  int scan[kSortWarps];
+};
+
+__global__ void __launch_bounds__(1024) group_rows_kernel(int n, int G, int stretch, const int32_t* __restrict__ ids,
                                                           int32_t* __restrict__ offsets, int32_t* __restrict__ rows) {
-  __shared__ int base[kMaxGroups + 1];
-  __shared__ int wtot[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int g = tid; g <= G; g += 1024) base[g] = 0;
+  extern __shared__ uint8_t raw[];
+  SortSide& s = *reinterpret_cast<SortSide*>(raw);
+  int* table = reinterpret_cast<int*>(raw + sizeof(SortSide));  // [warps][G + 1]
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, keys = G + 1;
+  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int i0 = min((rank * kSortWarps + warp) * stretch, n), i1 = min(i0 + stretch, n);
+  // warps that own a stretch: their tables are summed
+  const int left = n - rank * kSortWarps * stretch;
+  const int active = left <= 0 ? 0 : min((left + stretch - 1) / stretch, kSortWarps);
+  int* mine = table + warp * keys;
+  pdl_trigger();
+  for (int i = tid; i < active * keys; i += 1024) table[i] = 0;
+  pdl_wait();
   __syncthreads();
-  for (int i = tid; i < n; i += 1024) {
-    const int id = ids[i];
-    atomicAdd(&base[id >= 0 && id < G ? id : G], 1);
+  auto walk = [&](auto f) {
+    for (int b = i0; b < i1; b += 32 * kBatch) {
+      int key[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; j++) {
+        const int i = b + 32 * j + lane;
+        const int id = i < i1 ? ids[i] : 0;
+        key[j] = i < i1 ? (id >= 0 && id < G ? id : G) : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; j++) {
+        if (b + 32 * j >= i1) break;
+        const unsigned same = __match_any_sync(0xffffffffu, key[j]);
+        const int before = __popc(same & ((1u << lane) - 1u));
+        f(key[j], b + 32 * j + lane, before, __popc(same));
+        __syncwarp();
+      }
+    }
+  };
+  walk([&](int key, int, int before, int count) {
+    if (key >= 0 && before == 0) mine[key] += count;
+  });
+  __syncthreads();
+  // per group: the warps' counts to exclusive prefixes, and the CTA's total
+  for (int k = tid; k < keys; k += 1024) {
+    int run = 0;
+    for (int w = 0; w < active; w++) {
+      const int c = table[w * keys + k];
+      table[w * keys + k] = run;
+      run += c;
+    }
+    s.total[k] = run;
   }
-  __syncthreads();
-  // exclusive scan over the groups (G <= 1024, one per thread), then the rows of no group
-  const int c = tid < G ? base[tid] : 0;
-  int s = c;
+  if (ctas > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  // per group: rows in the CTAs before, and in all; then the groups' prefix
+  auto sums = [&](int k, int& below, int& all) {
+    below = all = 0;
+    for (int c = 0; c < ctas; c++) {
+      const int v = ctas > 1 ? *cluster.map_shared_rank(&s.total[k], c) : s.total[k];
+      if (c < rank) below += v;
+      all += v;
+    }
+  };
+  int below = 0, all = 0;
+  if (tid < G) sums(tid, below, all);
+  int none_below = 0, none_all = 0;
+  if (tid == 0) sums(G, none_below, none_all);
+  int inc = all;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += v;
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
   }
-  if (lane == 31) wtot[warp] = s;
-  __syncthreads();
-  int before = 0;
-  for (int w = 0; w < warp; w++) before += wtot[w];
-  __syncthreads();
+  if (lane == 31) s.scan[warp] = inc;
+  if (ctas > 1)
+    cluster.sync();  // the totals have been read everywhere
+  else
+    __syncthreads();
+  int run = inc - all, sum = 0;
+  for (int w = 0; w < kSortWarps; w++) {
+    if (w < warp) run += s.scan[w];
+    sum += s.scan[w];
+  }
   if (tid < G) {
-    base[tid] = before + s - c;
-    offsets[tid] = before + s - c;
-    if (tid == G - 1) {
-      base[G] = before + s;
-      offsets[G] = before + s;
-    }
+    s.total[tid] = run + below;
+    if (rank == 0) offsets[tid] = run;
+  }
+  if (tid == 0) {
+    s.total[G] = sum + none_below;
+    if (rank == 0) offsets[G] = sum;
   }
   __syncthreads();
-  for (int i0 = 0; i0 < n; i0 += 1024) {
-    const int i = i0 + tid;
-    const int id = i < n ? ids[i] : -1;
-    const int key = i < n ? (id >= 0 && id < G ? id : G) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, key);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    for (int w = 0; w < 32; w++) {
-      if (w == warp && key >= 0) {
-        rows[base[key] + rank] = i;
-        __syncwarp(__activemask());
-        if (rank == 0) base[key] += __popc(same);
-      }
-      __syncthreads();
+  walk([&](int key, int i, int before, int count) {
+    const int at = key >= 0 ? mine[key] : 0;
+    __syncwarp();
+    if (key >= 0) {
+      rows[s.total[key] + at + before] = i;
+      if (before == 0) mine[key] = at + count;
     }
-  }
+  });
 }
 
 }  // namespace
 
-cudaError_t launch_group_rows(int n, int n_groups, const int32_t* ids, int32_t* offsets, int32_t* rows, uint32_t*,
+cudaError_t launch_group_rows(int n, int n_groups, const int32_t* ids, int32_t* offsets, int32_t* rows,
                               cudaStream_t s) {
-  group_rows_kernel<<<1, 1024, 0, s>>>(n, n_groups, ids, offsets, rows);
-  return cudaGetLastError();
+  const int ctas = n <= 4096 ? 1 : 8;
+  const int stretch = ((n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
+  const int warps = n < kSortWarps * stretch ? (n + stretch - 1) / stretch : kSortWarps;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(1024);
+  cfg.dynamicSmemBytes = sizeof(SortSide) + sizeof(int) * (size_t)warps * (n_groups + 1);
+  if (cfg.dynamicSmemBytes > 48 * 1024) {
+    cudaError_t e =
+        cudaFuncSetAttribute(group_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
+  }
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, group_rows_kernel, n, n_groups, stretch, ids, offsets, rows);
 }
 
 }  // namespace moe

@@ -134,7 +134,7 @@ __device__ void lay_tiles(const TileArgs& a, Side& s) {
     const int g = tid * kPer + i;
     t[i] = 0;
     if (g < a.G) {
-      const int p0 = a.offsets[g], p1 = a.offsets[g + 1];
+      const int p0 = a.offsets ? a.offsets[g] : 0, p1 = a.offsets ? a.offsets[g + 1] : a.P;
       const bool fine = p0 >= 0 && p1 >= p0 && p1 <= a.P;
       bad |= !fine;
       s.first[g] = p0;
@@ -378,9 +378,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   const int u0 = blockIdx.x >> 1, du = gridDim.x >> 1;
   volatile int* stop = &s.stop;
 
-  if ((warp == 0 || (warp == 2 && (!a.gather || kMode == kAdapter))) && lane == 0) {
-    // ----------------------- boxes: the weights (warp 0), the rows (warp 2)
+  if ((warp == 0 || (warp == 2 && !a.gather)) && lane == 0) {
+    // ----------------------- boxes: the weights (warp 0), the rows (warp 2).
+    // Whoever waits on the ring waits for every stage in turn: a role that left
+    // stages out could fall two rounds behind, which a phase's parity hides.
     const bool rows = warp == 2;
+    bool z_ready = false;
     Turn it;
     int filled = 0;
     bool ok = true;
@@ -399,14 +402,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           at += 128 >> b;
         }
     };
-    if (kMode == kAdapter && rows) pdl_wait();
     for (int u = u0; u < w.units && ok; u += du) {
       const Tile t = tile_of<kMode>(a, s, w, u);
       const int half = ((t.n + 31) & ~31) >> 1, c0 = (t.c0 * 2 + rank) * kChan, p = t.p0 + rank * half;
       const uint32_t bytes = 2 * (kABytes + (a.gather ? 0 : half * 128));  // of both CTAs
       for (int kb = t.k0; kb < t.k1; kb++, it.next(a.stages), filled++) {
         const int k0 = kb * kBlockK;
-        if (kMode == kAdapter && rows) continue;  // gathered
         ok = wait_or_stop(&s.empty[it.st], it.round ^ 1, stop, a.err);
         if (!ok) break;
         uint8_t* A = ring + (size_t)it.st * a.stage_bytes;
@@ -432,18 +433,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           if (!wait_or_stop(&s.empty[it.st], it.round ^ 1, stop, a.err)) return false;
           uint8_t* A = ring + (size_t)it.st * a.stage_bytes;
           const uint32_t bar = full + it.st * 8;
-          if (rows) {
-            // rows of z: those of the column range, this CTA's half of them
-            const int hc = cols >> 1;
-            const int zr = g < a.G ? s.before[g] + t.p0 + c - (s.first[g] & ~31) + rank * hc : 0;
-            for (int i = 0; i < nh; i++)
-              fetch_rows(A + kABytes + i * hc * 128, maps.z, hc, [&](uint8_t* to, const CUtensorMap* m, int at) {
-                tma_3d(to, m, kb * kBlockK, zr + at, g < a.G ? h + i : 2, bar);  // 2: outside, zeros
-              });
-          } else {
-            if (rank == 0) mbar_expect_tx(&s.full[it.st], 2 * (kABytes + nh * (cols >> 1) * 128));
-            tma_3d(A, &maps.b, kb * kBlockK, c0, g, bar);  // adapter G: outside, zeros
-          }
+          if (rank == 0) mbar_expect_tx(&s.full[it.st], 2 * (kABytes + nh * (cols >> 1) * 128));
+          tma_3d(A, &maps.b, kb * kBlockK, c0, g, bar);  // adapter G: outside, zeros
+          if (!z_ready) pdl_wait();
+          z_ready = true;
+          // rows of z: those of the column range, this CTA's half of them
+          const int hc = cols >> 1;
+          const int zr = g < a.G ? s.before[g] + t.p0 + c - (s.first[g] & ~31) + rank * hc : 0;
+          for (int i = 0; i < nh; i++)
+            fetch_rows(A + kABytes + i * hc * 128, maps.z, hc, [&](uint8_t* to, const CUtensorMap* m, int at) {
+              tma_3d(to, m, kb * kBlockK, zr + at, g < a.G ? h + i : 2, bar);  // 2: outside, zeros
+            });
           it.next(a.stages);
           filled++;
           return true;

@@ -76,6 +76,8 @@ struct RouteArgs {
   const int32_t* expert_slot;  // [E] weight slot of each expert (< 0: none held), or null (slot = e)
 };
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
+// The router logits alone (into ws.logits), for any B.
+cudaError_t launch_logits(const RouteArgs& a, cudaStream_t s);
 
 struct ExpertArgs {
   int B, E, top_e, I, d, k, c, r;
@@ -156,7 +158,7 @@ constexpr int kMaxRows = 1 << 20;
 constexpr int kMaxWidth = 32768;
 
 cudaError_t launch_group_rows(int n, int n_groups, const int32_t* ids, int32_t* offsets, int32_t* rows,
-                              uint32_t* err, cudaStream_t s);
+                              cudaStream_t s);
 
 struct GroupedArgs {
   int G, P, n_x, n_y, N, K;
@@ -165,7 +167,7 @@ struct GroupedArgs {
   const uint16_t* x;        // [n_x, K]
   const int32_t* x_rows;    // [P] or null
   int x_div;
-  const int32_t* offsets;   // [G + 1]
+  const int32_t* offsets;   // [G + 1], or null: one group of all rows (G = 1)
   const uint16_t* w;        // the one matrix, or w_gate
   const uint16_t* w_up;     // null: a plain product
   void* y;                  // [n_y, N] bf16, or fp32 with y_fp32
@@ -213,7 +215,9 @@ struct BlockArgs {
   int32_t* ids_out;   // or null
   // workspace
   uint32_t* err;
-  double* logits;     // [B, E]
+  double* logits;     // [B, E] (B <= kExactTokens)
+  float* approx;      // [B, E] logits without bias, summed in fp32 (more tokens)
+  float* w_norm;      // [E] 2-norms of the router's rows
   int32_t* ids;       // [B, top_e]
   float* wts;         // [B, top_e]
   int32_t* offsets;   // [E + 1]

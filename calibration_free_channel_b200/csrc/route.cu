@@ -378,6 +378,13 @@ size_t workspace_layout(int B, int E, int top_e, int d, int I, int r, void* base
   return off;
 }
 
+cudaError_t launch_logits(const RouteArgs& a, cudaStream_t s) {
+  const int n_eblk = (a.E + kRouteExpertsPerCta - 1) / kRouteExpertsPerCta;
+  const int n_tblk = (a.B + kRouteTokensPerCta - 1) / kRouteTokensPerCta;
+  route_kernel<<<n_eblk * n_tblk, 256, 0, s>>>(a, n_eblk * n_tblk, n_eblk);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
   const int n_eblk = (a.E + kRouteExpertsPerCta - 1) / kRouteExpertsPerCta;
   const int n_tblk = (a.B + kRouteTokensPerCta - 1) / kRouteTokensPerCta;

@@ -272,6 +272,14 @@ def test_adapter_product_ranks(r, K, N):
     run_adapter(333, 3, K, N, r, ids_of(333, 3, "runs"), False, True, use_scale=False)
 
 
+@pytest.mark.parametrize("use_w,use_base", [(True, True), (False, True)])
+@pytest.mark.parametrize("kind", ["runs", "random", "all"])
+def test_adapter_product_many_tiles(kind, use_w, use_base):
+    # several tiles to a CTA pair, the ring going round many times between the adapters' stages
+    T = 3001
+    run_adapter(T, 5, 1096, 4096, 64, ids_of(T, 5, kind), use_w, use_base)
+
+
 def test_adapter_product_in_place():
     ids = ids_of(90, 7, "random")
     y = run_adapter(90, 7, 256, 512, 16, ids, False, True, inplace=True)
