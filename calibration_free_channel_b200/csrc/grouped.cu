@@ -14,7 +14,7 @@
 // warp 0 fetches boxes by bulk tensor copies into a ring of stages; warps
 // 8 .. 11 fetch the rows where they are gathered through the plan's row list
 // (16-byte copies; gathering bulk copies move four rows in about 80 cycles,
-// a third of the rate that the products need); one thread of the pair's first CTA issues the
+// a third of the rate that the products need); warp 1 of the pair's first CTA issues the
 // products; warps 4 .. 7 read the accumulator back, transform and store.  Two
 // accumulators let that overlap the next tile's products.
 //
@@ -339,7 +339,7 @@ template <int kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     tiles_kernel(const __grid_constant__ Maps maps, const TileArgs a) {
   extern __shared__ uint8_t raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = raw + (-smem_u32(raw) & 1023u);  // (an index: the compiler still sees shared memory)
   Side& s = *reinterpret_cast<Side*>(ring + (size_t)a.stages * a.stage_bytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x & 1;
   constexpr int kChan = kMode == kSwiglu ? kLanes / 2 : kLanes;  // output channels per CTA
@@ -378,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   const int u0 = blockIdx.x >> 1, du = gridDim.x >> 1;
   volatile int* stop = &s.stop;
 
-  if ((warp == 0 || (warp == 2 && !a.gather)) && lane == 0) {
+  if (warp == 0 || (warp == 2 && !a.gather)) {
     // ----------------------- boxes: the weights (warp 0), the rows (warp 2).
     // Whoever waits on the ring waits for every stage in turn: a role that left
     // stages out could fall two rounds behind, which a phase's parity hides.
@@ -408,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const uint32_t bytes = 2 * (kABytes + (a.gather ? 0 : half * 128));  // of both CTAs
       for (int kb = t.k0; kb < t.k1; kb++, it.next(a.stages), filled++) {
         const int k0 = kb * kBlockK;
-        ok = wait_or_stop(&s.empty[it.st], it.round ^ 1, stop, a.err);
+        ok = warp_wait(&s.empty[it.st], it.round ^ 1, stop, a.err);
         if (!ok) break;
         uint8_t* A = ring + (size_t)it.st * a.stage_bytes;
         const uint32_t bar = full + it.st * 8;
@@ -417,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                      [&](uint8_t* to, const CUtensorMap* m, int at) { tma_2d(to, m, k0, p + at, bar); });
           continue;
         }
-        if (rank == 0) mbar_expect_tx(&s.full[it.st], bytes);
+        if (rank == 0) mbar_expect(&s.full[it.st], bytes);
         if (kMode == kSwiglu) {
           tma_3d(A, &maps.w, k0, c0, t.g, bar);
           tma_3d(A + kABytes / 2, &maps.w_up, k0, c0, t.g, bar);
@@ -430,10 +430,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       }
       if (kMode == kAdapter && ok)
         ok = adapter_steps(a, s, w, t, [&](int g, int c, int cols, int kb, int h, int nh) {
-          if (!wait_or_stop(&s.empty[it.st], it.round ^ 1, stop, a.err)) return false;
+          if (!warp_wait(&s.empty[it.st], it.round ^ 1, stop, a.err)) return false;
           uint8_t* A = ring + (size_t)it.st * a.stage_bytes;
           const uint32_t bar = full + it.st * 8;
-          if (rank == 0) mbar_expect_tx(&s.full[it.st], 2 * (kABytes + nh * (cols >> 1) * 128));
+          if (rank == 0) mbar_expect(&s.full[it.st], 2 * (kABytes + nh * (cols >> 1) * 128));
           tma_3d(A, &maps.b, kb * kBlockK, c0, g, bar);  // adapter G: outside, zeros
           if (!z_ready) pdl_wait();
           z_ready = true;
@@ -450,41 +450,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         });
     }
     // after a timeout: the copies in flight must land before the pair ends
-    if (!ok && rank == 0)
+    if (!ok && rank == 0 && lane == 0)
       for (int i = filled > a.stages ? filled - a.stages : 0; i < filled; i++)
         mbar_wait_bounded(&s.full[i % a.stages], (i / a.stages) & 1, a.err);
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // -------------------------------------------------------- products
     Turn it;
     int ti = 0;
     bool ok = true;
+    // descriptors of the first stage; a stage, and a step of K, further
+    const bool mn_a = kMode == kPlain && a.layout;
+    const uint64_t a_desc = tile_desc(smem_u32(ring), mn_a ? kABytes / 2 : 16);
+    const uint64_t b_desc = tile_desc(smem_u32(ring) + kABytes, 16);
+    const int stage16 = a.stage_bytes >> 4;
+    const uint64_t a_step = mn_a ? 2048 >> 4 : 2;
     for (int u = u0; u < w.units && ok; u += du, ti++) {
       const Tile t = tile_of<kMode>(a, s, w, u);
       const uint32_t d = tmem + (ti & 1) * kMaxCols;
-      const bool mn_a = kMode == kPlain && a.layout;
       const uint32_t idesc = mma_desc(2 * kLanes, (t.n + 31) & ~31, mn_a);
-      ok = wait_or_stop(&s.acc_empty[ti & 1], ((ti >> 1) & 1) ^ 1, stop, a.err);
+      ok = warp_wait(&s.acc_empty[ti & 1], ((ti >> 1) & 1) ^ 1, stop, a.err);
       if (!ok) break;
       tc_fence_after();
       for (int kb = t.k0; kb < t.k1; kb++, it.next(a.stages)) {
-        ok = wait_or_stop(&s.full[it.st], it.round, stop, a.err);
+        ok = warp_wait(&s.full[it.st], it.round, stop, a.err);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t A = smem_u32(ring + (size_t)it.st * a.stage_bytes);
-        const uint64_t bd = tile_desc(A + kABytes, 16);
-        const int steps = (min(kBlockK, a.K - kb * kBlockK) + 15) / 16;  // past K the stage holds zeros
-        if (mn_a) {
-          const uint64_t ad = tile_desc(A, kABytes / 2);
-          for (int k = 0; k < steps; k++) mma_bf16(d, ad + k * (2048 >> 4), bd + k * 2, idesc, kb + k > t.k0);
-        } else {
-          const uint64_t ad = tile_desc(A, 16);
-          for (int k = 0; k < steps; k++) mma_bf16(d, ad + k * 2, bd + k * 2, idesc, kb + k > t.k0);
+        const uint64_t ad = a_desc + (uint64_t)(it.st * stage16), bd = b_desc + (uint64_t)(it.st * stage16);
+        const int left = a.K - kb * kBlockK;
+        if (left >= kBlockK) {
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; k++) mma_bf16(d, ad + k * a_step, bd + k * 2, idesc, kb > t.k0 || k > 0);
+        } else {  // past K the stage holds zeros
+          for (int k = 0; k * 16 < left; k++) mma_bf16(d, ad + k * a_step, bd + k * 2, idesc, kb > t.k0 || k > 0);
         }
         mma_commit(&s.empty[it.st]);
       }
       if (kMode == kAdapter && ok)
         ok = adapter_steps(a, s, w, t, [&](int g, int c, int cols, int kb, int h, int nh) {
-          if (!wait_or_stop(&s.full[it.st], it.round, stop, a.err)) return false;
+          if (!warp_wait(&s.full[it.st], it.round, stop, a.err)) return false;
           tc_fence_after();
           const uint32_t A = smem_u32(ring + (size_t)it.st * a.stage_bytes);
           const uint64_t ad = tile_desc(A, 16);
@@ -502,7 +505,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     }
     if (!ok) {  // after a timeout: the products in flight must end before the pair does
       mma_commit(&s.drain);
-      mbar_wait_bounded(&s.drain, 0, a.err);
+      if (lane == 0) mbar_wait_bounded(&s.drain, 0, a.err);
     }
   } else if (warp == 3 && lane == 0) {
     if (a.gather) announce_rows<kMode>(a, s, w);
@@ -593,7 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; i++) {
               const int q = q_of[i];
-              if (q >= 0 && c < a.N) y[(size_t)q * a.ldy + c] = f2bf16(r[i]);
+              st16_if(y + (size_t)q * a.ldy + c, f2bf16(r[i]), q >= 0 && c < a.N);
             }
           } else {
             const int c = cw + (lane & ~1);
@@ -603,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
               const float o = __shfl_xor_sync(0xffffffffu, odd ? r[i] : r[i + 1], 1);
               const uint32_t p2 = odd ? bf16x2(o, r[i + 1]) : bf16x2(r[i], o);
               const int q = q_of[i + (odd ? 1 : 0)];
-              if (q >= 0 && in_n) *reinterpret_cast<uint32_t*>(y + (size_t)q * a.ldy + c) = p2;
+              st32_if(y + (size_t)q * a.ldy + c, p2, q >= 0 && in_n);
             }
           }
         } else if (kMode == kPlain && a.y_fp32) {
@@ -613,7 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; j++) {
             const int q = s.y_row[(j & 1) * (kMaxCols / 2) + ((j0 + j) >> 1)];
-            if (q >= 0 && in_n) y[(size_t)q * a.ldy] = v[j];
+            st32_if(y + (size_t)q * a.ldy, __float_as_uint(v[j]), q >= 0 && in_n);
           }
         } else {
           // two channels to a word: the even lane of a pair takes the even column
@@ -628,7 +631,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           if (kMode == kAdapter && a.base) {
 #pragma unroll
             for (int i = 0; i < 16; i++)
-              bw[i] = qs[i] >= 0 && in_n ? *reinterpret_cast<const uint32_t*>(a.base + (size_t)qs[i] * a.ldy + c) : 0u;
+              bw[i] = ld32_if(a.base + (size_t)qs[i] * a.ldy + c, qs[i] >= 0 && in_n);
           }
 #pragma unroll
           for (int i = 0; i < 16; i++) {
@@ -638,7 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
               lo += bf16lo(bw[i]);
               hi += bf16hi(bw[i]);
             }
-            if (qs[i] >= 0 && in_n) *reinterpret_cast<uint32_t*>(y + (size_t)qs[i] * a.ldy) = bf16x2(lo, hi);
+            st32_if(y + (size_t)qs[i] * a.ldy, bf16x2(lo, hi), qs[i] >= 0 && in_n);
           }
         }
       }

@@ -27,17 +27,22 @@ __device__ __forceinline__ uint32_t mma_desc(int m, int n, bool mn_major_a) {
 // ----------------------------------------------------------------- tcgen05
 // All of these act on a pair of CTAs (a cluster of two): each holds half of
 // A's rows, half of B's and the accumulator of its own rows of A; one thread
-// of the pair's first CTA issues.
+// of the pair's first CTA issues.  What one thread issues is called by its
+// whole warp and issued by the lane that elect.sync names (always the same):
+// under `if (lane == 0)` the operands are not known to be the warp's, and an
+// issue took 78 cycles, so that a stage of four products took 800.
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n @e "
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
-// Arrives on `bar` of both CTAs when the MMAs this thread issued so far have completed.
+// Arrives on `bar` of both CTAs when the MMAs this warp issued so far have completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n @e "
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(
           smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
@@ -71,19 +76,29 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 // Tiled copies into this CTA's shared memory that complete on `bar`, a
-// shared::cluster address in either CTA of the pair.
+// shared::cluster address in either CTA of the pair (called by a whole warp).
 __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
   asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n @e "
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-      "%3}], [%4];" ::"r"(smem_u32(dst)),
+      "%3}], [%4];\n}" ::"r"(smem_u32(dst)),
       "l"(m), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
   asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n @e "
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-      "%3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "%3, %4}], [%5];\n}" ::"r"(smem_u32(dst)),
       "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// Arrives once and raises the phase's transaction count (called by a whole warp).
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(
+          smem_u32(bar)),
+      "r"(bytes)
       : "memory");
 }
 // 16 bytes global -> shared; `in` false writes zeros and reads nothing.
@@ -95,6 +110,26 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Stores and loads under a predicate: unrolled runs of them stay free of branches.
+__device__ __forceinline__ void st32_if(void* p, uint32_t v, bool on) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n @p st.global.b32 [%0], %1;\n}" ::"l"(p), "r"(v),
+               "r"((uint32_t)on)
+               : "memory");
+}
+__device__ __forceinline__ void st16_if(void* p, uint16_t v, bool on) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n @p st.global.b16 [%0], %1;\n}" ::"l"(p), "h"(v),
+               "r"((uint32_t)on)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t ld32_if(const void* p, bool on) {
+  uint32_t v;
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n mov.b32 %0, 0;\n @p ld.global.b32 %0, [%1];\n}"
+               : "=r"(v)
+               : "l"(p), "r"((uint32_t)on)
+               : "memory");
+  return v;
+}
 
 // ------------------------------------------------------------ bounded waits
 // Arrives on `bar`, a shared::cluster address of this CTA or its pair, with
@@ -121,6 +156,11 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
       : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
       : "memory");
   return ok != 0;
+}
+// The same for a whole warp: true for all lanes or for none.
+__device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop, uint32_t* err);
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* stop, uint32_t* err) {
+  return __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop, err));
 }
 // Waits for a phase; gives up (false) after kWaitLimitNs, recording the
 // timeout, or as soon as another role of the CTA has given up.
