@@ -3,7 +3,7 @@
 //
 // z has r <= 128 columns: 2 T r K multiply-adds against T K + r K inputs, so
 // it is bound by reading x and the adapters once, not by products.  One CTA
-// takes 16 sorted positions of one adapter; its 8 warps split K, each loading
+// takes 16 sorted positions of one adapter; its 16 warps split K (above rank 64 also the columns), each loading
 // 16-byte pieces of the rows of x and of A_g straight into the operands of
 // mma.sync (which values of K an operand slot holds is free, as long as x and
 // A_g agree: a thread's 8 consecutive values serve two products).
@@ -29,16 +29,18 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// kNT: tiles of 8 columns of z (r <= 8 kNT).
-template <int kNT>
-__global__ void __launch_bounds__(256) z_kernel(AdapterArgs a, size_t z_rows) {
-  extern __shared__ float red[];  // [8][kRowsZ][8 kNT]
-  __shared__ int first[kMaxGroups], before[kMaxGroups + 1], scan[8];
+// kNT: tiles of 8 columns of z that a warp computes; kHalves: 2 where the
+// columns are split over two sets of warps (r > 64).
+template <int kNT, int kHalves>
+__global__ void __launch_bounds__(512) z_kernel(AdapterArgs a, size_t z_rows) {
+  constexpr int kKWarps = 16 / kHalves, kCols = 8 * kNT * kHalves;
+  extern __shared__ float red[];  // [kKWarps][kRowsZ][kCols]
+  __shared__ int first[kMaxGroups], before[kMaxGroups + 1], scan[16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();  // what starts now finds everything earlier complete
   // the adapters' rows of z: the prefix of the padded row counts
-  constexpr int kPer = kMaxGroups / 256;
+  constexpr int kPer = kMaxGroups / 512;
   int n[kPer], sum = 0;
   bool bad = false;
 #pragma unroll
@@ -77,6 +79,7 @@ __global__ void __launch_bounds__(256) z_kernel(AdapterArgs a, size_t z_rows) {
   __syncthreads();
 
   const int units = before[a.A] / kRowsZ, r = a.r, gr = lane >> 2, t4 = lane & 3;
+  const int kw = warp % kKWarps, j0 = warp / kKWarps * 8 * kNT;  // this warp's share of K, its first column
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     int lo = 0, hi = a.A - 1;  // the last adapter with before[g] <= row
     while (lo < hi) {
@@ -109,8 +112,8 @@ __global__ void __launch_bounds__(256) z_kernel(AdapterArgs a, size_t z_rows) {
       }
       const uint16_t* A = a.a + (size_t)g * r * a.K;
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 2
-      for (int k0 = warp * 32; k0 < a.K; k0 += 256) {
+#pragma unroll(16 / kNT < 8 ? 16 / kNT : 8)
+      for (int k0 = kw * 32; k0 < a.K; k0 += 32 * kKWarps) {
         const int k = k0 + t4 * 8;
         const bool in = k < a.K;
         uint4 x0 = in && xr[0] ? __ldg(reinterpret_cast<const uint4*>(xr[0] + k)) : zero;
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(256) z_kernel(AdapterArgs a, size_t z_rows) {
         uint4 b[kNT];
 #pragma unroll
         for (int i = 0; i < kNT; i++) {
-          const int j = i * 8 + gr;
+          const int j = j0 + i * 8 + gr;
           b[i] = in && j < r ? __ldg(reinterpret_cast<const uint4*>(A + (size_t)j * a.K + k)) : zero;
         }
 #pragma unroll
@@ -129,22 +132,20 @@ __global__ void __launch_bounds__(256) z_kernel(AdapterArgs a, size_t z_rows) {
       }
     }
     // sum over the warps (their shares of K), in order
-    float* mine = red + warp * kRowsZ * 8 * kNT;
+    float* mine = red + kw * kRowsZ * kCols + j0;
 #pragma unroll
     for (int i = 0; i < kNT; i++) {
       const int j = i * 8 + 2 * t4;
-      mine[gr * 8 * kNT + j] = acc[i][0];
-      mine[gr * 8 * kNT + j + 1] = acc[i][1];
-      mine[(gr + 8) * 8 * kNT + j] = acc[i][2];
-      mine[(gr + 8) * 8 * kNT + j + 1] = acc[i][3];
+      *reinterpret_cast<float2*>(mine + gr * kCols + j) = make_float2(acc[i][0], acc[i][1]);
+      *reinterpret_cast<float2*>(mine + (gr + 8) * kCols + j) = make_float2(acc[i][2], acc[i][3]);
     }
     __syncthreads();
     const float scale = a.scale ? a.scale[g] : 1.0f;
-    for (int i = tid; i < kRowsZ * r; i += 256) {
+    for (int i = tid; i < kRowsZ * r; i += 512) {
       const int row = i / r, j = i - row * r;
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 8; w++) v += red[(w * kRowsZ + row) * 8 * kNT + j];
+      for (int w = 0; w < kKWarps; w++) v += red[(w * kRowsZ + row) * kCols + j];
       v *= scale;
       const uint16_t hi16 = f2bf16(v);
       const float left = v - bf16f(hi16);
@@ -162,16 +163,16 @@ cudaError_t launch_adapter_down(const AdapterArgs& a, cudaStream_t s) {
   const size_t zr = adapter_z_rows(a.T, a.A);
   const long units = (long)(zr / kRowsZ);  // at most
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units < 592 ? units : 592));  // four CTAs an SM
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)(units < 592 ? units : 592));  // twice what the SMs hold
+  cfg.blockDim = dim3(512);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto go = [&](auto kernel, int nt) {
-    cfg.dynamicSmemBytes = sizeof(float) * 8 * kRowsZ * 8 * nt;
+  auto go = [&](auto kernel, int floats) {
+    cfg.dynamicSmemBytes = sizeof(float) * kRowsZ * floats;
     if (cfg.dynamicSmemBytes > 32 * 1024) {
       cudaError_t e =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
@@ -179,7 +180,10 @@ cudaError_t launch_adapter_down(const AdapterArgs& a, cudaStream_t s) {
     }
     return cudaLaunchKernelEx(&cfg, kernel, a, zr);
   };
-  return a.r <= 16 ? go(z_kernel<2>, 2) : a.r <= 32 ? go(z_kernel<4>, 4) : a.r <= 64 ? go(z_kernel<8>, 8) : go(z_kernel<16>, 16);
+  if (a.r <= 16) return go(z_kernel<2, 1>, 16 * 16);
+  if (a.r <= 32) return go(z_kernel<4, 1>, 16 * 32);
+  if (a.r <= 64) return go(z_kernel<8, 1>, 16 * 64);
+  return go(z_kernel<8, 2>, 8 * 128);
 }
 
 }  // namespace moe

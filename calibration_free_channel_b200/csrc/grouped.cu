@@ -69,6 +69,7 @@ constexpr int kABytes = kLanes * kBlockK * 2;
 constexpr int kMaxStages = 8;
 constexpr int kMaxPairs = 74;              // CTA pairs of a launch
 constexpr int kMaxSplit = 8;               // parts of a tile's sum
+constexpr int kMinPart = 8;                // stages of K that a part has at least
 constexpr int kRowBoxes = 4;               // boxes of 128, 64, 32 and 16 rows
 constexpr int kSmemBudget = 227 * 1024 - 1024;  // 1024: the ring's alignment
 
@@ -82,6 +83,7 @@ struct Maps {
 struct TileArgs {
   int G, P, n_x, n_y, N, K, ldx, ldy;
   int cols;      // rows per tile at most (multiple of 32)
+  int b_rows;    // rows a stage has room for, per CTA
   int stages, stage_bytes;
   int layout, gather, x_div, y_fp32;
   int max_split;
@@ -182,7 +184,7 @@ __device__ __forceinline__ Walk walk_of(const TileArgs& a, const Side& s) {
   w.split = 1;
   if (tiles > 0 && 2 * tiles <= pairs) {
     w.split = min(a.max_split, pairs / tiles);
-    if (w.nkb) w.split = min(w.split, max(1, w.nkb / 2));  // two stages each at least
+    if (w.nkb) w.split = min(w.split, max(1, w.nkb / kMinPart));
   }
   w.units = tiles * w.split;
   return w;
@@ -250,7 +252,7 @@ __device__ __forceinline__ bool adapter_steps(const TileArgs& a, const Side& s, 
     if (s.rows[g] == 0) continue;
     const int c = max((s.first[g] & ~31) - t.p0, 0);
     const int cols = min(((s.first[g] + s.rows[g] + 31) & ~31) - t.p0, n) - c;
-    const int nh = cols <= a.cols / 2 ? 2 : 1;
+    const int nh = cols <= a.b_rows ? 2 : 1;
     for (int kb = 0; kb * kBlockK < a.r; kb++)
       for (int h = 0; h < 2; h += nh, e++)
         if (e % w.split == t.part && !f(g, c, cols, kb, h, nh)) return false;
@@ -565,10 +567,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         if (w.split > 1) {
 #pragma unroll
           for (int j = 0; j < 32; j++) v[j] = 0.0f;
-          for (int i = 0; i < w.split; i++) {
-            const float* p = part0 + i * part_size + j0 * kLanes;
+          // four columns at a time, all parts in flight; the sum in their order
+          const float* p = part0 + j0 * kLanes;
 #pragma unroll
-            for (int j = 0; j < 32; j++) v[j] += __ldcg(p + j * kLanes);
+          for (int j = 0; j < 32; j += 4) {
+            if (j0 + j >= t.n) break;
+            float x[kMaxSplit][4];
+#pragma unroll
+            for (int i = 0; i < kMaxSplit; i++)
+#pragma unroll
+              for (int k = 0; k < 4; k++)
+                x[i][k] = i < w.split ? __ldcg(p + i * part_size + (j + k) * kLanes) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kMaxSplit; i++)
+#pragma unroll
+              for (int k = 0; k < 4; k++) v[j + k] += x[i][k];
           }
         } else {
           tmem_ld32(acc + j0, v);
@@ -677,7 +690,9 @@ int most_cols(int n) { return n < kMaxCols ? (n + 31) / 32 * 32 : kMaxCols; }
 
 template <int kMode>
 cudaError_t run_tiles(const Maps& m, TileArgs t, cudaStream_t s) {
-  t.stage_bytes = kABytes + t.cols / 2 * 128;
+  // (32 at least: an adapter's narrowest columns with both halves of z)
+  t.b_rows = t.cols / 2 < 32 ? 32 : t.cols / 2;
+  t.stage_bytes = kABytes + t.b_rows * 128;
   t.stages = (kSmemBudget - (int)sizeof(Side)) / t.stage_bytes;
   if (t.stages > kMaxStages) t.stages = kMaxStages;
   t.max_split = kMaxSplit;
