@@ -27,6 +27,8 @@
 // further stages: A is B_g, B the rows of z = scale x A_g^T (adapter.cu), the
 // accumulator's columns those of the adapter, widened to multiples of 32 with
 // zero rows.  So the low-rank term costs its own bytes and products only.
+// For many tokens z itself comes from these tiles (kLowRank: W_g = A_g, and a
+// group's range of positions widened as z's is).
 //
 // A call with few tiles splits their sums over K: each part is written in
 // fp32, and the CTA that arrives last adds them in order and finishes the tile.
@@ -69,11 +71,13 @@ constexpr int kABytes = kLanes * kBlockK * 2;
 constexpr int kMaxStages = 8;
 constexpr int kMaxPairs = 74;              // CTA pairs of a launch
 constexpr int kMaxSplit = 8;               // parts of a tile's sum
+constexpr int kLowRankCols = 64;           // rows per tile of z
+constexpr int kFewTokens = 512;            // up to here z comes from adapter.cu
 constexpr int kMinPart = 8;                // stages of K that a part has at least
 constexpr int kRowBoxes = 4;               // boxes of 128, 64, 32 and 16 rows
 constexpr int kSmemBudget = 227 * 1024 - 1024;  // 1024: the ring's alignment
 
-enum Mode { kPlain, kSwiglu, kAdapter };
+enum Mode { kPlain, kSwiglu, kAdapter, kLowRank };
 
 struct Maps {
   CUtensorMap x[kRowBoxes], w, w_up;
@@ -98,6 +102,8 @@ struct TileArgs {
   // adapters (G of them; the tiles run over all P rows)
   int r, has_w;
   const uint16_t* base;
+  const float* scale;     // kLowRank
+  size_t z_half;          // elements of one of z's halves
 };
 
 // Shared memory behind the ring.
@@ -105,12 +111,13 @@ struct Side {
   uint64_t full[kMaxStages], landed[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int stop, tiles, last;
-  int scan[kGThreads / 32];
+  unsigned long long scan[kGThreads / 32];
   alignas(16) int y_row[kMaxCols];  // result row of each column, -1: none; even columns, then odd ones
   float swap[2][2][2][16][32];      // [quarter][turn][from the up side][column][lane]
   int first[kMaxGroups];            // first sorted position of each group
   int rows[kMaxGroups];             // rows of each group
-  int before[kMaxGroups + 1];       // row tiles of the groups before (adapters: rows of z before)
+  int before[kMaxGroups];           // row tiles of the groups before (adapters: rows of z before)
+  int z_before[kMaxGroups];         // kLowRank: rows of z before
 };
 
 // A role's place in the ring: the stage, and how often it has gone round.
@@ -129,41 +136,49 @@ template <int kMode>
 __device__ void lay_tiles(const TileArgs& a, Side& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kPer = (kMaxGroups + kGThreads - 1) / kGThreads;
-  int t[kPer], sum = 0;
+  constexpr bool kZ = kMode == kAdapter || kMode == kLowRank;  // z's rows are counted too
+  int t[kPer], z[kPer];
+  unsigned long long sum = 0;  // row tiles, and rows of z in the high half
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kPer; i++) {
     const int g = tid * kPer + i;
-    t[i] = 0;
+    t[i] = z[i] = 0;
     if (g < a.G) {
       const int p0 = a.offsets ? a.offsets[g] : 0, p1 = a.offsets ? a.offsets[g + 1] : a.P;
       const bool fine = p0 >= 0 && p1 >= p0 && p1 <= a.P;
       bad |= !fine;
-      s.first[g] = p0;
-      s.rows[g] = fine ? p1 - p0 : 0;
-      if (fine) t[i] = kMode == kAdapter ? padded_rows(p0, p1) : (p1 - p0 + a.cols - 1) / a.cols;
+      if (fine && kZ) z[i] = padded_rows(p0, p1);
+      const int rows = !fine ? 0 : kMode == kLowRank ? z[i] : p1 - p0;
+      s.first[g] = kMode == kLowRank ? p0 & ~31 : p0;
+      s.rows[g] = rows;
+      t[i] = (rows + a.cols - 1) / a.cols;
     }
-    sum += t[i];
+    sum += (unsigned)t[i] | (unsigned long long)z[i] << 32;
   }
-  int inc = sum;
+  unsigned long long inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    const unsigned long long v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
   if (lane == 31) s.scan[warp] = inc;
   bad = __syncthreads_or(bad);
-  int run = inc - sum;
+  unsigned long long run = inc - sum;
   for (int w = 0; w < warp; w++) run += s.scan[w];
+  int tiles = (int)run, zr = (int)(run >> 32);
 #pragma unroll
   for (int i = 0; i < kPer; i++) {
     const int g = tid * kPer + i;
-    if (g < a.G) s.before[g] = run;
-    run += t[i];
+    if (g < a.G) {
+      s.before[g] = kMode == kAdapter ? zr : tiles;
+      if (kMode == kLowRank) s.z_before[g] = zr;
+    }
+    tiles += t[i];
+    zr += z[i];
     if (g == a.G - 1) {
-      s.before[a.G] = run;
-      if (kMode == kAdapter) run = (a.P + a.cols - 1) / a.cols;
-      s.tiles = bad ? 0 : run;  // offsets that do not ascend within the rows: nothing is computed
+      if (kMode == kAdapter) tiles = (a.P + a.cols - 1) / a.cols;  // over all rows
+      s.tiles = bad ? 0 : tiles;  // offsets that do not ascend within the rows: nothing is computed
       if (bad) atomicOr(a.err, kErrBadPlan);
     }
   }
@@ -247,15 +262,18 @@ __device__ __forceinline__ bool adapter_steps(const TileArgs& a, const Side& s, 
     else
       lo = m + 1;
   }
-  int e = 0;
+  int skip = t.part;
   for (int g = lo; g < a.G && s.first[g] < t.p0 + t.n; g++) {
     if (s.rows[g] == 0) continue;
     const int c = max((s.first[g] & ~31) - t.p0, 0);
     const int cols = min(((s.first[g] + s.rows[g] + 31) & ~31) - t.p0, n) - c;
     const int nh = cols <= a.b_rows ? 2 : 1;
     for (int kb = 0; kb * kBlockK < a.r; kb++)
-      for (int h = 0; h < 2; h += nh, e++)
-        if (e % w.split == t.part && !f(g, c, cols, kb, h, nh)) return false;
+      for (int h = 0; h < 2; h += nh, skip--)
+        if (skip == 0) {
+          skip = w.split;
+          if (!f(g, c, cols, kb, h, nh)) return false;
+        }
   }
   return true;
 }
@@ -276,10 +294,11 @@ __device__ void gather_rows(const TileArgs& a, Side& s, uint8_t* ring, const Wal
     const uint16_t* src[8];
 #pragma unroll
     for (int m = 0; m < 8; m++) {
-      // rows past the tile's end repeat its last one (their columns are not stored)
+      // rows past the tile's end repeat its last one (their columns are not
+      // stored, or as zeros)
       int row = 0;
       if (r0 + 16 * m < half) {
-        row = a.x_rows[tl.p0 + min(rank * half + r0 + 16 * m, tl.n - 1)];
+        row = a.x_rows[min(tl.p0 + min(rank * half + r0 + 16 * m, tl.n - 1), a.P - 1)];
         row = row < 0 ? -1 : row / a.x_div;
         if (row < 0 || row >= a.n_x) {
           atomicOr(a.err, kErrBadPlan);
@@ -364,12 +383,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     if (kMode == kAdapter) tma_prefetch(&maps.b);
   }
   if (warp == 2) tmem_alloc(&s.tmem, 512);
-  // Adapters: the launch before this one (adapter.cu) lets it start only once
-  // everything earlier has completed, so only z, which it writes, is waited for.
-  if (kMode != kAdapter) {
-    pdl_trigger();
-    pdl_wait();
-  }
+  // Adapters: the launch before this one, of z, lets it start only once
+  // everything earlier has completed, so only z is waited for.
+  if (kMode != kAdapter && kMode != kLowRank) pdl_trigger();
+  if (kMode != kAdapter) pdl_wait();
+  if (kMode == kLowRank) pdl_trigger();
   tc_fence_before();
   lay_tiles<kMode>(a, s);
   cluster_arrive();
@@ -522,7 +540,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const Tile t = tile_of<kMode>(a, s, w, u);
       for (int j = et; j < ((t.n + 31) & ~31); j += 128) {
         int q = -1;
-        if (j < t.n) {
+        if (kMode == kLowRank) {
+          // row q of z, or of zeros (-2 - q) where the adapter does not own the position
+          const int p = t.p0 + j;
+          if (j < t.n) {
+            q = s.z_before[t.g] + p - s.first[t.g];
+            const bool own = p >= a.offsets[t.g] && p < a.offsets[t.g + 1];
+            const int row = own ? a.x_rows[p] : -1;
+            if (row < 0 || row >= a.n_x) q = -2 - q;
+          }
+        } else if (j < t.n) {
           q = a.y_rows ? a.y_rows[t.p0 + j] : t.p0 + j;
           if (q < 0 || q >= a.n_y) {
             atomicOr(a.err, kErrBadPlan);
@@ -631,6 +658,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             const int q = s.y_row[(j & 1) * (kMaxCols / 2) + ((j0 + j) >> 1)];
             st32_if(y + (size_t)q * a.ldy, __float_as_uint(v[j]), q >= 0 && in_n);
           }
+        } else if (kMode == kLowRank) {
+          // the value and what its rounding leaves, two channels to a word
+          const int c = q4 * 32 + (lane & ~1);
+          const bool in_n = rank == 0 && c < a.N;
+          const float scale = a.scale ? a.scale[t.g] : 1.0f;
+          uint16_t* z = static_cast<uint16_t*>(a.y) + c;
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            const float o = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+            int q = s.y_row[(odd ? kMaxCols / 2 : 0) + (j0 >> 1) + i];
+            const bool own = q >= 0, some = q != -1;
+            if (!own) q = -2 - q;
+            const float lo = own ? (odd ? o : v[2 * i]) * scale : 0.0f, hi = own ? (odd ? v[2 * i + 1] : o) * scale : 0.0f;
+            const uint32_t top = bf16x2(lo, hi);
+            // (an infinity leaves no rest)
+            const float rl = isfinite(lo) ? lo - bf16lo(top) : 0.0f, rh = isfinite(hi) ? hi - bf16hi(top) : 0.0f;
+            st32_if(z + (size_t)q * a.N, top, some && in_n);
+            st32_if(z + a.z_half + (size_t)q * a.N, bf16x2(rl, rh), some && in_n);
+          }
         } else {
           // two channels to a word: the even lane of a pair takes the even column
           const int c = (t.c0 * 2 + rank) * kChan + q4 * 32 + (lane & ~1);
@@ -695,7 +741,7 @@ cudaError_t run_tiles(const Maps& m, TileArgs t, cudaStream_t s) {
   t.stage_bytes = kABytes + t.b_rows * 128;
   t.stages = (kSmemBudget - (int)sizeof(Side)) / t.stage_bytes;
   if (t.stages > kMaxStages) t.stages = kMaxStages;
-  t.max_split = kMaxSplit;
+  t.max_split = kMode == kLowRank ? 1 : kMaxSplit;
   const size_t smem = 1024 + (size_t)t.stages * t.stage_bytes + sizeof(Side);
   cudaError_t e = cudaFuncSetAttribute(tiles_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -706,7 +752,7 @@ cudaError_t run_tiles(const Maps& m, TileArgs t, cudaStream_t s) {
   const long n_ct = (t.N + chan - 1) / chan;
   // units at most: the tiles, each in as many parts as there may be
   long most = (long)(t.P + t.cols - 1) / t.cols;
-  if (kMode != kAdapter) most += t.G < t.P ? t.G : t.P;
+  if (kMode != kAdapter) most += 2 * (t.G < t.P ? t.G : t.P);
   most *= n_ct * kMaxSplit;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * (most < pairs ? most : pairs)));
@@ -785,8 +831,34 @@ cudaError_t launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   return a.w_up ? run_tiles<kSwiglu>(m, t, s) : run_tiles<kPlain>(m, t, s);
 }
 
+// z on the tensor cores, for many tokens.
+static cudaError_t launch_low_rank(const AdapterArgs& a, cudaStream_t s) {
+  TileArgs t = {};
+  t.G = a.A;
+  t.P = t.n_x = a.T;
+  t.N = a.r;
+  t.K = t.ldx = a.K;
+  t.gather = 1;
+  t.x_div = 1;
+  t.x = a.x;
+  t.x_rows = a.rows;
+  t.offsets = a.offsets;
+  t.y = a.z;
+  t.err = a.err;
+  t.scale = a.scale;
+  t.z_half = adapter_z_rows(a.T, a.A) * a.r;
+  t.cols = kLowRankCols;
+  Maps m;
+  memset(&m, 0, sizeof m);
+  const uint64_t K = a.K, r = a.r;
+  if (!row_maps(m.x, a.x, K, a.T, 0, 2 * K, 0) ||
+      !tensor_map(&m.w, a.a, K, r, a.A, 2 * K, 2 * K * r, kBlockK, kLanes))
+    return cudaErrorInvalidValue;
+  return run_tiles<kLowRank>(m, t, s);
+}
+
 cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s) {
-  cudaError_t e = launch_adapter_down(a, s);
+  cudaError_t e = a.T <= kFewTokens ? launch_adapter_down(a, s) : launch_low_rank(a, s);
   if (e != cudaSuccess) return e;
   TileArgs t = {};
   t.G = a.A;
