@@ -138,7 +138,7 @@ cudaError_t launch_group_rows(int n, int n_groups, const int32_t* ids, int32_t* 
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(1024);
   cfg.dynamicSmemBytes = sizeof(SortSide) + sizeof(int) * (size_t)warps * (n_groups + 1);
-  if (cfg.dynamicSmemBytes > 48 * 1024) {
+  if (cfg.dynamicSmemBytes > 40 * 1024) {
     cudaError_t e =
         cudaFuncSetAttribute(group_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return e;

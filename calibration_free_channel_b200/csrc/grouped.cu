@@ -34,8 +34,6 @@
 // fp32, and the CTA that arrives last adds them in order and finishes the tile.
 #include <cudaTypedefs.h>
 
-#include <cstring>
-
 #include "kernels.h"
 #include "tensor.cuh"
 
@@ -377,7 +375,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     mbar_init(&s.drain, 1);
     s.stop = 0;
     fence_mbar_init();
-    for (int i = 0; i < kRowBoxes; i++) tma_prefetch(kMode == kAdapter ? &maps.z[i] : &maps.x[i]);
+    if (kMode == kAdapter || !a.gather)
+      for (int i = 0; i < kRowBoxes; i++) tma_prefetch(kMode == kAdapter ? &maps.z[i] : &maps.x[i]);
     tma_prefetch(&maps.w);
     if (kMode == kSwiglu) tma_prefetch(&maps.w_up);
     if (kMode == kAdapter) tma_prefetch(&maps.b);
@@ -718,15 +717,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   if (kMode == kAdapter) pdl_wait();  // whoever waits for this launch waits for the one before it too
 }
 
-int sm_count() {
-  static thread_local int dev_of = -1, count = 0;
+// What a device answered once: its SM count, and which kernels have been
+// given their shared memory on it.
+struct DeviceState {
+  int dev = -1, sms = 0;
+  bool allowed[4] = {};
+};
+cudaError_t device_state(DeviceState** out) {
+  static thread_local DeviceState state;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev != dev_of) {
-    if (cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    dev_of = dev;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev != state.dev) {
+    state = DeviceState();
+    e = cudaDeviceGetAttribute(&state.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    state.dev = dev;
   }
-  return count;
+  *out = &state;
+  return state.sms < 2 ? cudaErrorInvalidDevice : cudaSuccess;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -743,11 +752,14 @@ cudaError_t run_tiles(const Maps& m, TileArgs t, cudaStream_t s) {
   if (t.stages > kMaxStages) t.stages = kMaxStages;
   t.max_split = kMode == kLowRank ? 1 : kMaxSplit;
   const size_t smem = 1024 + (size_t)t.stages * t.stage_bytes + sizeof(Side);
-  cudaError_t e = cudaFuncSetAttribute(tiles_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  DeviceState* dev = nullptr;
+  cudaError_t e = device_state(&dev);
+  if (e == cudaSuccess && !dev->allowed[kMode]) {
+    e = cudaFuncSetAttribute(tiles_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget + 1024);
+    dev->allowed[kMode] = e == cudaSuccess;
+  }
   if (e != cudaSuccess) return e;
-  const int sms = sm_count();
-  if (sms < 2) return cudaErrorInvalidDevice;
-  const int pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
+  const int pairs = dev->sms / 2 < kMaxPairs ? dev->sms / 2 : kMaxPairs;
   const int chan = kMode == kSwiglu ? kLanes : 2 * kLanes;
   const long n_ct = (t.N + chan - 1) / chan;
   // units at most: the tiles, each in as many parts as there may be
@@ -817,10 +829,9 @@ cudaError_t launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   t.count = static_cast<uint32_t*>(a.split);
   t.part = reinterpret_cast<float*>(static_cast<char*>(a.split) + align256(sizeof(uint32_t) * 2 * kMaxPairs));
   t.cols = choose_cols(a.P, a.G < a.P ? a.G : a.P, a.N, a.w_up ? kLanes : 2 * kLanes);
-  Maps m;
-  memset(&m, 0, sizeof m);
+  Maps m;  // (what a mode does not use stays unset)
   const uint64_t N = a.N, K = a.K;
-  bool ok = row_maps(m.x, a.x, K, a.n_x, 0, 2ull * a.ldx, 0);
+  bool ok = t.gather || row_maps(m.x, a.x, K, a.n_x, 0, 2ull * a.ldx, 0);
   if (a.w_up)
     ok = ok && tensor_map(&m.w, a.w, K, N, a.G, 2 * K, 2 * N * K, kBlockK, kLanes / 2) &&
          tensor_map(&m.w_up, a.w_up, K, N, a.G, 2 * K, 2 * N * K, kBlockK, kLanes / 2);
@@ -831,35 +842,29 @@ cudaError_t launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   return a.w_up ? run_tiles<kSwiglu>(m, t, s) : run_tiles<kPlain>(m, t, s);
 }
 
-// z on the tensor cores, for many tokens.
-static cudaError_t launch_low_rank(const AdapterArgs& a, cudaStream_t s) {
-  TileArgs t = {};
-  t.G = a.A;
-  t.P = t.n_x = a.T;
-  t.N = a.r;
-  t.K = t.ldx = a.K;
-  t.gather = 1;
-  t.x_div = 1;
-  t.x = a.x;
-  t.x_rows = a.rows;
-  t.offsets = a.offsets;
-  t.y = a.z;
-  t.err = a.err;
-  t.scale = a.scale;
-  t.z_half = adapter_z_rows(a.T, a.A) * a.r;
-  t.cols = kLowRankCols;
-  Maps m;
-  memset(&m, 0, sizeof m);
-  const uint64_t K = a.K, r = a.r;
-  if (!row_maps(m.x, a.x, K, a.T, 0, 2 * K, 0) ||
-      !tensor_map(&m.w, a.a, K, r, a.A, 2 * K, 2 * K * r, kBlockK, kLanes))
-    return cudaErrorInvalidValue;
-  return run_tiles<kLowRank>(m, t, s);
-}
-
 cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s) {
-  cudaError_t e = a.T <= kFewTokens ? launch_adapter_down(a, s) : launch_low_rank(a, s);
-  if (e != cudaSuccess) return e;
+  const uint64_t N = a.N, K = a.K, r = a.r, zr = adapter_z_rows(a.T, a.A);
+  // z on the tensor cores, for many tokens
+  const bool many = a.T > kFewTokens;
+  TileArgs z = {};
+  Maps mz;
+  if (many) {
+    z.G = a.A;
+    z.P = z.n_x = a.T;
+    z.N = a.r;
+    z.K = z.ldx = a.K;
+    z.gather = 1;
+    z.x_div = 1;
+    z.x = a.x;
+    z.x_rows = a.rows;
+    z.offsets = a.offsets;
+    z.y = a.z;
+    z.err = a.err;
+    z.scale = a.scale;
+    z.z_half = zr * a.r;
+    z.cols = kLowRankCols;
+    if (!tensor_map(&mz.w, a.a, K, r, a.A, 2 * K, 2 * K * r, kBlockK, kLanes)) return cudaErrorInvalidValue;
+  }
   TileArgs t = {};
   t.G = a.A;
   t.P = t.n_x = t.n_y = a.T;
@@ -879,14 +884,14 @@ cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s) {
   t.base = a.base;
   t.cols = choose_cols(a.T, 1, a.N, 2 * kLanes);
   Maps m;
-  memset(&m, 0, sizeof m);
-  const uint64_t N = a.N, K = a.K, r = a.r, zr = adapter_z_rows(a.T, a.A);
   const bool ok = row_maps(m.z, a.z, r, zr, 2, 2 * r, 2 * r * zr) &&
                   tensor_map(&m.b, a.b, r, N, a.A, 2 * r, 2 * r * N, kBlockK, kLanes) &&
                   (!a.w || tensor_map(&m.w, a.w, K, N, 1, 2 * K, 2 * N * K, kBlockK, kLanes));
   if (!ok) return cudaErrorInvalidValue;
   if (!a.w) m.w = m.b;
-  return run_tiles<kAdapter>(m, t, s);
+  // (the maps are ready, so that the second launch follows the first at once)
+  const cudaError_t e = many ? run_tiles<kLowRank>(mz, z, s) : launch_adapter_down(a, s);
+  return e == cudaSuccess ? run_tiles<kAdapter>(m, t, s) : e;
 }
 
 }  // namespace moe

@@ -123,7 +123,9 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        # the current stream's handle without building a Stream object (which costs more than a launch);
+        # before torch has set CUDA up, that is the default stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if torch.cuda.is_initialized() else None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
