@@ -40,7 +40,7 @@
 namespace moe {
 
 bool tensor_map(CUtensorMap* m, const void* base, uint64_t x, uint64_t y, uint64_t z, uint64_t row_bytes,
-                uint64_t mat_bytes, uint32_t box_x, uint32_t box_y) {
+                uint64_t mat_bytes, uint32_t box_x, uint32_t box_y, uint32_t box_z) {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -53,7 +53,7 @@ bool tensor_map(CUtensorMap* m, const void* base, uint64_t x, uint64_t y, uint64
   }();
   if (!encode) return false;
   const cuuint64_t dims[3] = {x, y, z}, strides[2] = {row_bytes, mat_bytes};
-  const cuuint32_t box[3] = {box_x, box_y, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {box_x, box_y, box_z}, step[3] = {1, 1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, z ? 3 : 2, const_cast<void*>(base), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -79,7 +79,7 @@ enum Mode { kPlain, kSwiglu, kAdapter, kLowRank };
 
 struct Maps {
   CUtensorMap x[kRowBoxes], w, w_up;
-  CUtensorMap z[kRowBoxes], b;  // adapters
+  CUtensorMap z[kRowBoxes], z2, b;  // adapters (z2: 16 rows of both halves)
 };
 
 struct TileArgs {
@@ -96,7 +96,7 @@ struct TileArgs {
   void* y;
   uint32_t* err;
   uint32_t* count;        // [kMaxPairs][2] arrivals of a split tile's parts
-  float* part;            // [kMaxPairs][2][cols][128] the parts
+  float* part;            // [kMaxPairs][2][cols / 4][128][4] the parts (four columns of a lane together)
   // adapters (G of them; the tiles run over all P rows)
   int r, has_w;
   const uint16_t* base;
@@ -247,12 +247,13 @@ __device__ __forceinline__ Tile tile_of(const TileArgs& a, const Side& s, const 
 // columns [c, c + w) of the tile, block kb of its rank, and nh of z's two
 // halves from h (both where they fit into a stage).  Without a projection the
 // first is a stage of zeros (g = G) that sets the whole accumulator.  A split
-// tile's parts take them in turn.  f returns whether to go on.
+// tile's parts share its adapters.  f returns whether to go on.
 template <typename F>
 __device__ __forceinline__ bool adapter_steps(const TileArgs& a, const Side& s, const Walk& w, const Tile& t, F f) {
   const int n = (t.n + 31) & ~31;
   if (!a.has_w && !f(a.G, 0, n, 0, 0, 1)) return false;
-  int lo = 0, hi = a.G;  // the first adapter that ends behind p0
+  // the first adapter that ends behind position p, and the first that begins at or behind it
+  int lo = 0, hi = a.G;
   while (lo < hi) {
     const int m = (lo + hi) >> 1;
     if (s.first[m] + s.rows[m] > t.p0)
@@ -260,18 +261,28 @@ __device__ __forceinline__ bool adapter_steps(const TileArgs& a, const Side& s, 
     else
       lo = m + 1;
   }
-  int skip = t.part;
-  for (int g = lo; g < a.G && s.first[g] < t.p0 + t.n; g++) {
-    if (s.rows[g] == 0) continue;
-    const int c = max((s.first[g] & ~31) - t.p0, 0);
-    const int cols = min(((s.first[g] + s.rows[g] + 31) & ~31) - t.p0, n) - c;
+  int end = a.G;
+  for (int low = lo; low < end;) {
+    const int m = (low + end) >> 1;
+    if (s.first[m] >= t.p0 + t.n)
+      end = m;
+    else
+      low = m + 1;
+  }
+  if (w.split > 1) {
+    const int all = end - lo;
+    end = lo + all * (t.part + 1) / w.split;
+    lo += all * t.part / w.split;
+  }
+  for (int g = lo; g < end; g++) {
+    const int first = s.first[g], rows = s.rows[g];
+    if (rows == 0) continue;
+    const int c = max((first & ~31) - t.p0, 0);
+    const int cols = min(((first + rows + 31) & ~31) - t.p0, n) - c;
     const int nh = cols <= a.b_rows ? 2 : 1;
     for (int kb = 0; kb * kBlockK < a.r; kb++)
-      for (int h = 0; h < 2; h += nh, skip--)
-        if (skip == 0) {
-          skip = w.split;
-          if (!f(g, c, cols, kb, h, nh)) return false;
-        }
+      for (int h = 0; h < 2; h += nh)
+        if (!f(g, c, cols, kb, h, nh)) return false;
   }
   return true;
 }
@@ -351,6 +362,38 @@ __device__ void announce_rows(const TileArgs& a, Side& s, const Walk& w) {
     if (kMode == kAdapter &&
         !adapter_steps(a, s, w, t, [&](int, int, int, int, int, int) { return pass_on(); }))
       return;
+  }
+}
+
+// The sum of the parts, in their order, of 32 columns (the first n of them):
+// kCols columns at a time with all of their loads in flight.
+template <int kParts, int kCols>
+__device__ __forceinline__ void add_parts(const float* p, size_t stride, int parts, int n, float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; j += kCols) {
+    float4 x[kParts][kCols / 4];
+#pragma unroll
+    for (int i = 0; i < kParts; i++)
+#pragma unroll
+      for (int k = 0; k < kCols / 4; k++)
+        x[i][k] = i < parts && j + 4 * k < n
+                      ? __ldcg(reinterpret_cast<const float4*>(p + i * stride + (j + 4 * k) * kLanes))
+                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kCols / 4; k++) {
+      float4 s = x[0][k];
+#pragma unroll
+      for (int i = 1; i < kParts; i++) {
+        s.x += x[i][k].x;
+        s.y += x[i][k].y;
+        s.z += x[i][k].z;
+        s.w += x[i][k].w;
+      }
+      v[j + 4 * k] = s.x;
+      v[j + 4 * k + 1] = s.y;
+      v[j + 4 * k + 2] = s.z;
+      v[j + 4 * k + 3] = s.w;
+    }
   }
 }
 
@@ -459,8 +502,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           // rows of z: those of the column range, this CTA's half of them
           const int hc = cols >> 1;
           const int zr = g < a.G ? s.before[g] + t.p0 + c - (s.first[g] & ~31) + rank * hc : 0;
-          for (int i = 0; i < nh; i++)
-            fetch_rows(A + kABytes + i * hc * 128, maps.z, hc, [&](uint8_t* to, const CUtensorMap* m, int at) {
+          if (nh == 2 && hc == 16)
+            tma_3d(A + kABytes, &maps.z2, kb * kBlockK, zr, 0, bar);
+          else
+            for (int i = 0; i < nh; i++)
+              fetch_rows(A + kABytes + i * hc * 128, maps.z, hc, [&](uint8_t* to, const CUtensorMap* m, int at) {
               tma_3d(to, m, kb * kBlockK, zr + at, g < a.G ? h + i : 2, bar);  // 2: outside, zeros
             });
           it.next(a.stages);
@@ -567,14 +613,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const uint32_t acc = tmem + ((uint32_t)(q4 * 32) << 16) + (ti & 1) * kMaxCols;
       bool finish = true;
       const size_t part_size = (size_t)2 * a.cols * kLanes;
-      float* part0 = a.part + (size_t)t.index * w.split * part_size + (size_t)rank * a.cols * kLanes + q4 * 32 + lane;
+      float* part0 = a.part + (size_t)t.index * w.split * part_size + (size_t)rank * a.cols * kLanes + (q4 * 32 + lane) * 4;
       if (w.split > 1) {
         float* mine = part0 + t.part * part_size;
         for (int j0 = 0; j0 < t.n; j0 += 32) {
           float v[32];
           tmem_ld32(acc + j0, v);
 #pragma unroll
-          for (int j = 0; j < 32; j++) __stcg(mine + (j0 + j) * kLanes, v[j]);
+          for (int j = 0; j < 32; j += 4)
+            __stcg(reinterpret_cast<float4*>(mine + (j0 + j) * kLanes), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
         }
         __threadfence();
         bar_any(1, 128, false);
@@ -591,24 +638,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       for (int j0 = 0; j0 < t.n && finish; j0 += 32) {
         float v[32];
         if (w.split > 1) {
-#pragma unroll
-          for (int j = 0; j < 32; j++) v[j] = 0.0f;
-          // four columns at a time, all parts in flight; the sum in their order
-          const float* p = part0 + j0 * kLanes;
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            if (j0 + j >= t.n) break;
-            float x[kMaxSplit][4];
-#pragma unroll
-            for (int i = 0; i < kMaxSplit; i++)
-#pragma unroll
-              for (int k = 0; k < 4; k++)
-                x[i][k] = i < w.split ? __ldcg(p + i * part_size + (j + k) * kLanes) : 0.0f;
-#pragma unroll
-            for (int i = 0; i < kMaxSplit; i++)
-#pragma unroll
-              for (int k = 0; k < 4; k++) v[j + k] += x[i][k];
-          }
+          if (w.split <= 4)
+            add_parts<4, 16>(part0 + j0 * kLanes, part_size, w.split, t.n - j0, v);
+          else
+            add_parts<kMaxSplit, 8>(part0 + j0 * kLanes, part_size, w.split, t.n - j0, v);
         } else {
           tmem_ld32(acc + j0, v);
         }
@@ -885,6 +918,7 @@ cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s) {
   t.cols = choose_cols(a.T, 1, a.N, 2 * kLanes);
   Maps m;
   const bool ok = row_maps(m.z, a.z, r, zr, 2, 2 * r, 2 * r * zr) &&
+                  tensor_map(&m.z2, a.z, r, zr, 2, 2 * r, 2 * r * zr, kBlockK, 16, 2) &&
                   tensor_map(&m.b, a.b, r, N, a.A, 2 * r, 2 * r * N, kBlockK, kLanes) &&
                   (!a.w || tensor_map(&m.w, a.w, K, N, 1, 2 * K, 2 * N * K, kBlockK, kLanes));
   if (!ok) return cudaErrorInvalidValue;

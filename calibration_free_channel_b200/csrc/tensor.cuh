@@ -192,6 +192,6 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool say) {
 // bf16 matrices [z][y][x] with row and matrix strides in bytes (multiples of
 // 16), 128-byte swizzle, zeros outside.  Returns false on failure.
 bool tensor_map(CUtensorMap* m, const void* base, uint64_t x, uint64_t y, uint64_t z, uint64_t row_bytes,
-                uint64_t mat_bytes, uint32_t box_x, uint32_t box_y);
+                uint64_t mat_bytes, uint32_t box_x, uint32_t box_y, uint32_t box_z = 1);
 
 }  // namespace moe
