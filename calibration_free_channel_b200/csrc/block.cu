@@ -17,26 +17,39 @@ constexpr int kExactTokens = 32;  // up to here every logit is summed in fp64
 // the tokens; there the tensor cores compute logits with fp32 sums (exact
 // products), which are off by at most
 //   delta = d 2^-23 |x| |w_e|  (2-norms)
-// (every partial sum is bounded by |x| |w_e|, and a step of 16 products rounds
-// 17 terms).  Experts whose fp32 logits are more than 2 delta apart are in the
+// and a sixteenth more (every partial sum is bounded by |x| |w_e|, and a step
+// of 16 products cuts 17 terms).  Experts whose fp32 logits are more than 2 delta apart are in the
 // right order; the others near or above the last chosen place are computed
 // again in fp64, and the order of the candidates is decided by that.
-__device__ __forceinline__ double dot64(const uint16_t* x, const uint16_t* w, int d, int lane) {
-  double s = 0.0;
+__device__ __forceinline__ void dot64x2(const uint16_t* x, const uint16_t* w0, const uint16_t* w1, int d, int lane,
+                                        double& s0, double& s1) {
+  s0 = s1 = 0.0;
+#pragma unroll 4
   for (int k = lane * 8; k < d; k += 256) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k)), b = __ldg(reinterpret_cast<const uint4*>(w + k));
-    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k)), b = __ldg(reinterpret_cast<const uint4*>(w0 + k)),
+                c = __ldg(reinterpret_cast<const uint4*>(w1 + k));
+    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w}, cv[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
     for (int i = 0; i < 4; i++) {  // products of two bf16 are exact in fp32
-      s += (double)(bf16lo(av[i]) * bf16lo(bv[i]));
-      s += (double)(bf16hi(av[i]) * bf16hi(bv[i]));
+      s0 += (double)(bf16lo(av[i]) * bf16lo(bv[i]));
+      s0 += (double)(bf16hi(av[i]) * bf16hi(bv[i]));
+      s1 += (double)(bf16lo(av[i]) * bf16lo(cv[i]));
+      s1 += (double)(bf16hi(av[i]) * bf16hi(cv[i]));
     }
   }
-  return warp_sum(s);
+  s0 = warp_sum(s0);
+  s1 = warp_sum(s1);
+}
+
+// A logit that is not a number ranks last (the token's weights are NaN then).
+template <typename V>
+__device__ __forceinline__ V ranked(V v) {
+  return v == v ? v : (V)-INFINITY;
 }
 
 __device__ __forceinline__ float norm2(const uint16_t* x, int d, int lane) {
   float s = 0.0f;
+#pragma unroll 4
   for (int k = lane * 8; k < d; k += 256) {
     const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k));
     const uint32_t av[4] = {a.x, a.y, a.z, a.w};
@@ -75,65 +88,76 @@ __device__ __forceinline__ void put_choice(const BlockArgs& a, int t, int rank, 
   }
 }
 
-// The largest `most` of E values (value(e), every lane may ask for any of its
-// e = lane + 32 m), in order, ties to the lower id: lane s gets the s-th, as
-// long as more(s, value) says so before it is taken.  Returns how many.
-template <typename V, typename F, typename M>
-__device__ __forceinline__ int take_largest(int E, int lane, int most, F value, M more, V& mine, int& my_id) {
-  uint32_t taken = 0;
-  int s = 0;
-  for (; s < most; s++) {
-    V bv = -INFINITY;
-    int bi = 0x7fffffff;
-    for (int m = 0; lane + 32 * m < E; m++) {
-      if (taken & (1u << m)) continue;
-      const V v = value(lane + 32 * m);
-      if (bi == 0x7fffffff || v > bv) {
-        bv = v;
-        bi = lane + 32 * m;
-      }
+// Takes the largest of the values that the lanes hold (expert lane + 32 m in
+// v[m]), ties to the lower id; `taken` marks this lane's that are gone.
+template <int kM, typename V>
+__device__ __forceinline__ void largest(const V (&v)[kM], int E, int lane, uint32_t& taken, V& best, int& id) {
+  best = -INFINITY;
+  id = 0x7fffffff;
+#pragma unroll
+  for (int m = 0; m < kM; m++)
+    if (lane + 32 * m < E && !(taken >> m & 1) && (id == 0x7fffffff || v[m] > best)) {
+      best = v[m];
+      id = lane + 32 * m;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const V ov = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-      if (oi != 0x7fffffff && (bi == 0x7fffffff || ov > bv || (ov == bv && oi < bi))) {
-        bv = ov;
-        bi = oi;
-      }
-    }
-    if (bi == 0x7fffffff || !more(s, bv)) break;
-    if ((bi & 31) == lane) taken |= 1u << (bi >> 5);
-    if (lane == s) {
-      mine = bv;
-      my_id = bi;
+  for (int o = 16; o > 0; o >>= 1) {
+    const V ov = __shfl_xor_sync(0xffffffffu, best, o);
+    const int oi = __shfl_xor_sync(0xffffffffu, id, o);
+    if (oi != 0x7fffffff && (id == 0x7fffffff || ov > best || (ov == best && oi < id))) {
+      best = ov;
+      id = oi;
     }
   }
-  return s;
+  if ((id & 31) == lane && id != 0x7fffffff) taken |= 1u << (id >> 5);
 }
 
-// One warp per token.  kExact: the logits are fp64 already.
-template <bool kExact>
+// The logits of two experts for token x, in fp64.
+__device__ __forceinline__ void exact_logits(const BlockArgs& a, const uint16_t* x, int e0, int e1, int lane,
+                                             double& l0, double& l1) {
+  dot64x2(x, a.w_router + (size_t)e0 * a.d, a.w_router + (size_t)e1 * a.d, a.d, lane, l0, l1);
+  l0 = ranked(l0 + (a.bias ? (double)a.bias[e0] : 0.0));
+  l1 = ranked(l1 + (a.bias ? (double)a.bias[e1] : 0.0));
+}
+
+// One warp per token, E <= 32 kM.  kExact: the logits are fp64 already.
+template <int kM, bool kExact>
 __global__ void __launch_bounds__(256) choose_kernel(BlockArgs a) {
   const int lane = threadIdx.x & 31, t = blockIdx.x * 8 + (threadIdx.x >> 5);
   pdl_trigger();
   pdl_wait();
   if (t >= a.B) return;
+  uint32_t taken = 0;
+  int id = 0;
   if (kExact) {
-    const double* L = a.logits + (size_t)t * a.E;
-    double v = 0.0;
-    int id = 0;
-    const int n = take_largest(
-        a.E, lane, a.top_e, [&](int e) { return L[e]; }, [](int, double) { return true; }, v, id);
-    put_choice(a, t, lane < n ? lane : -1, id, v);
+    double v[kM], mine = 0.0;
+#pragma unroll
+    for (int m = 0; m < kM; m++)
+      v[m] = lane + 32 * m < a.E ? ranked(a.logits[(size_t)t * a.E + lane + 32 * m]) : 0.0;
+    for (int s = 0; s < a.top_e; s++) {
+      double best;
+      int e;
+      largest(v, a.E, lane, taken, best, e);
+      if (lane == s) {
+        mine = best;
+        id = e;
+      }
+    }
+    put_choice(a, t, lane < a.top_e ? lane : -1, id, mine);
     return;
   }
-  const float* L = a.approx + (size_t)t * a.E;
   const uint16_t* x = a.x + (size_t)t * a.d;
-  float w_max = 0.0f, l_max = 0.0f;
-  for (int e = lane; e < a.E; e += 32) {
-    w_max = fmaxf(w_max, a.w_norm[e]);
-    l_max = fmaxf(l_max, fabsf(L[e]) + (a.bias ? fabsf(a.bias[e]) : 0.0f));
+  float v[kM], w_max = 0.0f, l_max = 0.0f;
+#pragma unroll
+  for (int m = 0; m < kM; m++) {
+    const int e = lane + 32 * m;
+    v[m] = 0.0f;
+    if (e < a.E) {
+      const float l = a.approx[(size_t)t * a.E + e], b = a.bias ? a.bias[e] : 0.0f;
+      v[m] = ranked(l + b);
+      w_max = fmaxf(w_max, a.w_norm[e]);
+      l_max = fmaxf(l_max, fabsf(l) + fabsf(b));
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -141,44 +165,66 @@ __global__ void __launch_bounds__(256) choose_kernel(BlockArgs a) {
     l_max = fmaxf(l_max, __shfl_xor_sync(0xffffffffu, l_max, o));
   }
   // the sum's error, and the bias's addition
-  const float apart = 2.0f * ((float)a.d * 0x1p-23f * norm2(x, a.d, lane) * w_max + 0x1p-23f * l_max);
-  float v = 0.0f, last = 0.0f;
-  int id = 0;
-  const int n = take_largest(
-      a.E, lane, 32, [&](int e) { return L[e] + (a.bias ? a.bias[e] : 0.0f); },
-      [&](int s, float b) {
-        if (s < a.top_e) last = b;
-        return s < a.top_e || last - b <= apart;
-      },
-      v, id);
-  if (n == 32 && a.E > 32) {
-    // too many near the border (equal rows, a token of zeros): all of them in fp64
-    double all[32];
-    for (int e = 0; e < a.E; e++) {
-      const double s = dot64(x, a.w_router + (size_t)e * a.d, a.d, lane) + (a.bias ? (double)a.bias[e] : 0.0);
-      if ((e & 31) == lane) all[e >> 5] = s;
+  const float apart = 2.0f * (1.0625f * (float)a.d * 0x1p-23f * norm2(x, a.d, lane) * w_max + 0x1p-23f * l_max);
+  // the chosen by these logits, in order, one to a lane, and behind them
+  // those within reach of the last
+  float mine = 0.0f, last = 0.0f;
+  int n = 0;
+  for (; n < 32 && n < a.E; n++) {
+    float best;
+    int e;
+    largest(v, a.E, lane, taken, best, e);
+    if (n >= a.top_e && !(last - best <= apart)) break;
+    if (n < a.top_e) last = best;
+    if (lane == n) {
+      mine = best;
+      id = e;
     }
-    double w = 0.0;
-    const int k = take_largest(
-        a.E, lane, a.top_e, [&](int e) { return all[e >> 5]; }, [](int, double) { return true; }, w, id);
-    put_choice(a, t, lane < k ? lane : -1, id, w);
+  }
+  if (n == 32 && a.E > 32) {
+    // too many within reach (equal rows, a token of zeros): all of them in fp64
+    double all[kM], got = 0.0;
+#pragma unroll
+    for (int m = 0; m < kM; m++) {
+      all[m] = 0.0;
+      for (int l = 0; l < 32 && l + 32 * m < a.E; l += 2) {
+        double s0, s1;
+        exact_logits(a, x, l + 32 * m, min(l + 1 + 32 * m, a.E - 1), lane, s0, s1);
+        if (l == lane) all[m] = s0;
+        if (l + 1 == lane) all[m] = s1;
+      }
+    }
+    taken = 0;
+    for (int s = 0; s < a.top_e; s++) {
+      double best;
+      int e;
+      largest(all, a.E, lane, taken, best, e);
+      if (lane == s) {
+        got = best;
+        id = e;
+      }
+    }
+    put_choice(a, t, lane < a.top_e ? lane : -1, id, got);
     return;
   }
-  const float up = __shfl_up_sync(0xffffffffu, v, 1), down = __shfl_down_sync(0xffffffffu, v, 1);
-  const bool near = lane < n && ((lane > 0 && !(up - v > apart)) || (lane + 1 < n && !(v - down > apart)));
-  double exact = (double)v;
-  for (unsigned todo = __ballot_sync(0xffffffffu, near); todo; todo &= todo - 1) {
-    const int s = __ffs(todo) - 1, e = __shfl_sync(0xffffffffu, id, s);
-    const double l = dot64(x, a.w_router + (size_t)e * a.d, a.d, lane) + (a.bias ? (double)a.bias[e] : 0.0);
-    if (lane == s) exact = l;
+  const float up = __shfl_up_sync(0xffffffffu, mine, 1), down = __shfl_down_sync(0xffffffffu, mine, 1);
+  const bool near = lane < n && ((lane > 0 && !(up - mine > apart)) || (lane + 1 < n && !(mine - down > apart)));
+  double exact = (double)mine;
+  for (unsigned todo = __ballot_sync(0xffffffffu, near); todo;) {  // two at a time
+    const int s0 = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int s1 = todo ? __ffs(todo) - 1 : s0;
+    todo &= todo - 1;
+    double l0, l1;
+    exact_logits(a, x, __shfl_sync(0xffffffffu, id, s0), __shfl_sync(0xffffffffu, id, s1), lane, l0, l1);
+    if (lane == s0) exact = l0;
+    if (lane == s1) exact = l1;
   }
   int rank = 0;
   for (int s = 0; s < n; s++) {
     const double o = __shfl_sync(0xffffffffu, exact, s);
     const int oi = __shfl_sync(0xffffffffu, id, s);
-    // (a NaN counts as the largest: whatever the order, the ranks stay distinct)
-    const bool mine_nan = exact != exact, o_nan = o != o;
-    if (o_nan || mine_nan ? (o_nan && (!mine_nan || oi < id)) : (o > exact || (o == exact && oi < id))) rank++;
+    if (o > exact || (o == exact && oi < id)) rank++;
   }
   put_choice(a, t, lane < n ? rank : -1, id, exact);
 }
@@ -265,6 +311,7 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
     cfg.gridDim = dim3(grid);
     return cudaLaunchKernelEx(&cfg, kernel, a);
   };
+  const int by8 = (a.B + 7) / 8;
   cudaError_t e;
   if (a.B <= kExactTokens) {
     RouteArgs r = {};
@@ -276,7 +323,8 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
     r.bias = a.bias;
     r.ws.logits = a.logits;
     e = launch_logits(r, s);
-    if (e == cudaSuccess) e = launch(choose_kernel<true>, (a.B + 7) / 8);
+    if (e == cudaSuccess)
+      e = a.E <= 128 ? launch(choose_kernel<4, true>, by8) : launch(choose_kernel<32, true>, by8);
   } else {
     e = launch(norms_kernel, (a.E + 7) / 8);
     if (e != cudaSuccess) return e;
@@ -293,7 +341,8 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
     l.err = a.err;
     l.split = a.split;
     e = launch_grouped(l, s);
-    if (e == cudaSuccess) e = launch(choose_kernel<false>, (a.B + 7) / 8);
+    if (e == cudaSuccess)
+      e = a.E <= 128 ? launch(choose_kernel<4, false>, by8) : launch(choose_kernel<32, false>, by8);
   }
   if (e != cudaSuccess) return e;
   e = launch_group_rows(P, a.E, a.ids, a.offsets, a.rows, s);

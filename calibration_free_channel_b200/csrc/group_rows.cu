@@ -18,6 +18,7 @@ namespace moe {
 namespace {
 
 constexpr int kSortWarps = 32;
+constexpr int kSortCtas = 8;
 constexpr int kBatch = 8;  // ids a lane loads at a time
 
 struct SortSide {
@@ -25,7 +26,7 @@ struct SortSide {
   int scan[kSortWarps];
 };
 
-__global__ void __launch_bounds__(1024) group_rows_kernel(int n, int G, int stretch, const int32_t* __restrict__ ids,
+__global__ void __launch_bounds__(1024) group_rows_kernel(int n, int G, int bits, int stretch, const int32_t* __restrict__ ids,
                                                           int32_t* __restrict__ offsets, int32_t* __restrict__ rows) {
   extern __shared__ uint8_t raw[];
   SortSide& s = *reinterpret_cast<SortSide*>(raw);
@@ -54,7 +55,14 @@ __global__ void __launch_bounds__(1024) group_rows_kernel(int n, int G, int stre
 #pragma unroll
       for (int j = 0; j < kBatch; j++) {
         if (b + 32 * j >= i1) break;
-        const unsigned same = __match_any_sync(0xffffffffu, key[j]);
+        // lanes with the same key, a ballot for each bit of it (match.any takes
+        // a step for each distinct key: 1900 cycles instead of 150 for 32 of them)
+        unsigned same = __ballot_sync(0xffffffffu, key[j] >= 0);
+        for (int bit = 0; bit < bits; bit++) {
+          const bool on = (key[j] >> bit) & 1;
+          const unsigned m = __ballot_sync(0xffffffffu, on);
+          same &= on ? m : ~m;
+        }
         const int before = __popc(same & ((1u << lane) - 1u));
         f(key[j], b + 32 * j + lane, before, __popc(same));
         __syncwarp();
@@ -68,10 +76,15 @@ __global__ void __launch_bounds__(1024) group_rows_kernel(int n, int G, int stre
   // per group: the warps' counts to exclusive prefixes, and the CTA's total
   for (int k = tid; k < keys; k += 1024) {
     int run = 0;
-    for (int w = 0; w < active; w++) {
-      const int c = table[w * keys + k];
-      table[w * keys + k] = run;
-      run += c;
+    for (int w0 = 0; w0 < active; w0 += 8) {
+      int c[8];
+#pragma unroll
+      for (int w = 0; w < 8; w++) c[w] = w0 + w < active ? table[(w0 + w) * keys + k] : 0;
+#pragma unroll
+      for (int w = 0; w < 8; w++) {
+        if (w0 + w < active) table[(w0 + w) * keys + k] = run;
+        run += c[w];
+      }
     }
     s.total[k] = run;
   }
@@ -80,18 +93,27 @@ __global__ void __launch_bounds__(1024) group_rows_kernel(int n, int G, int stre
   else
     __syncthreads();
   // per group: rows in the CTAs before, and in all; then the groups' prefix
-  auto sums = [&](int k, int& below, int& all) {
-    below = all = 0;
-    for (int c = 0; c < ctas; c++) {
-      const int v = ctas > 1 ? *cluster.map_shared_rank(&s.total[k], c) : s.total[k];
-      if (c < rank) below += v;
-      all += v;
+  // (thread k has group k, the last thread the rows of no group as well)
+  int below = 0, all = 0, none_below = 0;
+  auto sums = [&](int k, int& lo, int& sum) {
+    if (ctas == 1) {
+      sum = s.total[k];
+      return;
+    }
+    int c[kSortCtas];
+#pragma unroll
+    for (int i = 0; i < kSortCtas; i++) c[i] = *cluster.map_shared_rank(&s.total[k], i);
+#pragma unroll
+    for (int i = 0; i < kSortCtas; i++) {
+      if (i < rank) lo += c[i];
+      sum += c[i];
     }
   };
-  int below = 0, all = 0;
   if (tid < G) sums(tid, below, all);
-  int none_below = 0, none_all = 0;
-  if (tid == 0) sums(G, none_below, none_all);
+  if (tid == 1023) {
+    int none = 0;
+    sums(G, none_below, none);
+  }
   int inc = all;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -103,16 +125,19 @@ __global__ void __launch_bounds__(1024) group_rows_kernel(int n, int G, int stre
     cluster.sync();  // the totals have been read everywhere
   else
     __syncthreads();
-  int run = inc - all, sum = 0;
-  for (int w = 0; w < kSortWarps; w++) {
-    if (w < warp) run += s.scan[w];
-    sum += s.scan[w];
+  int warps = s.scan[lane];  // every warp scans the warps' sums
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, warps, o);
+    if (lane >= o) warps += v;
   }
+  const int sum = __shfl_sync(0xffffffffu, warps, 31);
+  const int run = (warp ? __shfl_sync(0xffffffffu, warps, warp - 1) : 0) + inc - all;
   if (tid < G) {
     s.total[tid] = run + below;
     if (rank == 0) offsets[tid] = run;
   }
-  if (tid == 0) {
+  if (tid == 1023) {
     s.total[G] = sum + none_below;
     if (rank == 0) offsets[G] = sum;
   }
@@ -131,9 +156,11 @@ __global__ void __launch_bounds__(1024) group_rows_kernel(int n, int G, int stre
 
 cudaError_t launch_group_rows(int n, int n_groups, const int32_t* ids, int32_t* offsets, int32_t* rows,
                               cudaStream_t s) {
-  const int ctas = n <= 4096 ? 1 : 8;
+  const int ctas = n <= 4096 ? 1 : kSortCtas;
   const int stretch = ((n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
   const int warps = n < kSortWarps * stretch ? (n + stretch - 1) / stretch : kSortWarps;
+  int bits = 1;
+  while (n_groups >> bits) bits++;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(1024);
@@ -152,7 +179,7 @@ cudaError_t launch_group_rows(int n, int n_groups, const int32_t* ids, int32_t* 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, group_rows_kernel, n, n_groups, stretch, ids, offsets, rows);
+  return cudaLaunchKernelEx(&cfg, group_rows_kernel, n, n_groups, bits, stretch, ids, offsets, rows);
 }
 
 }  // namespace moe

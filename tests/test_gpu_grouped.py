@@ -427,6 +427,13 @@ def test_block_nan_token_stays_apart():
     keep = [i for i in range(50) if i != 9]
     assert torch.equal(y[keep], z[keep])
     assert not bool(torch.isfinite(z[9]).any())
+    # the experts of such a token are still experts, each once (few tokens and many)
+    for B in (20, 50):
+        x2[3] = float("inf")
+        ids = torch.full((B, 2), -1, dtype=torch.int32, device="cuda")
+        L.forward_grouped(x2[:B], ids=ids)
+        L.check()
+        assert ((ids >= 0) & (ids < 8)).all() and (ids[:, 0] != ids[:, 1]).all()
 
 
 # ------------------------------------------------------------- bad plans
