@@ -63,12 +63,15 @@ __device__ __forceinline__ float norm2(const uint16_t* x, int d, int lane) {
 }
 
 __global__ void __launch_bounds__(256) norms_kernel(BlockArgs a) {
+  // beside the logits' launch, which lets this one start when everything
+  // earlier is complete
   const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   pdl_trigger();
-  pdl_wait();
-  if (e >= a.E) return;
-  const float n = norm2(a.w_router + (size_t)e * a.d, a.d, lane);
-  if (lane == 0) a.w_norm[e] = n;
+  if (e < a.E) {
+    const float n = norm2(a.w_router + (size_t)e * a.d, a.d, lane);
+    if (lane == 0) a.w_norm[e] = n;
+  }
+  pdl_wait();  // whoever waits for this launch waits for the logits too
 }
 
 // The chosen experts of a token, one to a lane (rank -1: none), with their
@@ -326,8 +329,6 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
     if (e == cudaSuccess)
       e = a.E <= 128 ? launch(choose_kernel<4, true>, by8) : launch(choose_kernel<32, true>, by8);
   } else {
-    e = launch(norms_kernel, (a.E + 7) / 8);
-    if (e != cudaSuccess) return e;
     GroupedArgs l = {};
     l.G = 1;
     l.P = l.n_x = l.n_y = a.B;
@@ -340,7 +341,9 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
     l.y_fp32 = 1;
     l.err = a.err;
     l.split = a.split;
+    l.late_trigger = 1;
     e = launch_grouped(l, s);
+    if (e == cudaSuccess) e = launch(norms_kernel, (a.E + 7) / 8);
     if (e == cudaSuccess)
       e = a.E <= 128 ? launch(choose_kernel<4, false>, by8) : launch(choose_kernel<32, false>, by8);
   }

@@ -69,7 +69,6 @@ constexpr int kABytes = kLanes * kBlockK * 2;
 constexpr int kMaxStages = 8;
 constexpr int kMaxPairs = 74;              // CTA pairs of a launch
 constexpr int kMaxSplit = 8;               // parts of a tile's sum
-constexpr int kLowRankCols = 64;           // rows per tile of z
 constexpr int kFewTokens = 512;            // up to here z comes from adapter.cu
 constexpr int kMinPart = 8;                // stages of K that a part has at least
 constexpr int kRowBoxes = 4;               // boxes of 128, 64, 32 and 16 rows
@@ -89,6 +88,7 @@ struct TileArgs {
   int stages, stage_bytes;
   int layout, gather, x_div, y_fp32;
   int max_split;
+  int late_trigger;       // the next launch starts once everything before this one is complete
   const uint16_t* x;
   const int32_t* x_rows;
   const int32_t* offsets;
@@ -328,7 +328,7 @@ __device__ void gather_rows(const TileArgs& a, Side& s, uint8_t* ring, const Wal
       const bool in = kb * kBlockK + piece * 8 < a.K;
 #pragma unroll
       for (int m = 0; m < 8; m++)
-        if (r0 + 16 * m < half) cp_async16(dst + m * 2048, in ? src[m] + kb * kBlockK : a.x, in);
+        cp_async16_if(dst + m * 2048, src[m] + (in ? kb * kBlockK : 0), in, r0 + 16 * m < half);
       cp_async_arrive(&s.landed[it.st]);
     }
     if (kMode == kAdapter && ok)  // nothing to copy, but the stage is announced like any other
@@ -427,9 +427,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   if (warp == 2) tmem_alloc(&s.tmem, 512);
   // Adapters: the launch before this one, of z, lets it start only once
   // everything earlier has completed, so only z is waited for.
-  if (kMode != kAdapter && kMode != kLowRank) pdl_trigger();
-  if (kMode != kAdapter) pdl_wait();
-  if (kMode == kLowRank) pdl_trigger();
+  if (kMode != kAdapter) {
+    if (!a.late_trigger) pdl_trigger();
+    pdl_wait();
+    if (a.late_trigger) pdl_trigger();
+  }
   tc_fence_before();
   lay_tiles<kMode>(a, s);
   cluster_arrive();
@@ -826,6 +828,14 @@ int choose_cols(int n, int groups, int N, int chan) {
   return cols;
 }
 
+// Rows per tile of z: as few as leave each CTA pair one tile at most (an
+// adapter's widened range adds up to one and a half).
+int low_rank_cols(int T, int A) {
+  const int left = kMaxPairs - 3 * (A < kMaxPairs / 6 ? A : kMaxPairs / 6) / 2;
+  const int cols = ((T + left - 1) / left + 31) / 32 * 32;
+  return cols < kMaxCols ? cols : kMaxCols;
+}
+
 bool row_maps(CUtensorMap* m, const void* base, uint64_t x, uint64_t y, uint64_t z, uint64_t row_bytes,
               uint64_t mat_bytes) {
   for (int b = 0; b < kRowBoxes; b++)
@@ -853,6 +863,7 @@ cudaError_t launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   t.gather = a.x_rows != nullptr;
   t.x_div = a.x_div;
   t.y_fp32 = a.y_fp32;
+  t.late_trigger = a.late_trigger;
   t.x = a.x;
   t.x_rows = a.x_rows;
   t.offsets = a.offsets;
@@ -895,7 +906,8 @@ cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s) {
     z.err = a.err;
     z.scale = a.scale;
     z.z_half = zr * a.r;
-    z.cols = kLowRankCols;
+    z.late_trigger = 1;
+    z.cols = low_rank_cols(a.T, a.A);
     if (!tensor_map(&mz.w, a.a, K, r, a.A, 2 * K, 2 * K * r, kBlockK, kLanes)) return cudaErrorInvalidValue;
   }
   TileArgs t = {};

@@ -173,6 +173,7 @@ struct GroupedArgs {
   void* y;                  // [n_y, N] bf16, or fp32 with y_fp32
   int y_fp32;
   const int32_t* y_rows;    // [P] or null
+  int late_trigger;         // 1: the next launch may rely on all launches before this one
   uint32_t* err;
   void* split;              // split_bytes(P) of workspace, zero before first use
 };

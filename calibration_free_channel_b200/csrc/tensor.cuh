@@ -101,9 +101,11 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
       "r"(bytes)
       : "memory");
 }
-// 16 bytes global -> shared; `in` false writes zeros and reads nothing.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+// 16 bytes global -> shared, or zeros (`in` false: nothing is read), where `on`.
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool in, bool on) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n @p cp.async.cg.shared.global [%0], [%1], 16, %2;\n}" ::"r"(dst),
+               "l"(src), "r"(in ? 16 : 0), "r"((uint32_t)on)
+               : "memory");
 }
 // Arrives on `bar` (one of its expected arrivals) when this thread's copies so far have completed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
