@@ -261,6 +261,14 @@ __global__ void __launch_bounds__(256) combine_kernel(BlockArgs a) {
   }
 }
 
+// The SwiGLU values go to the second product as bf16, which adds as much error
+// to the result as its own rounding does.  While an expert has 64 tokens or
+// fewer on average they are held in two bf16 terms, 16 significant bits: the
+// second product is bound by its weights there, and the second term's rows and
+// products cost nothing that shows.  Above that they would: half of the
+// block's products again.
+bool two_terms(int B, int E, int top_e) { return (long)B * top_e <= 64L * E; }
+
 // row stride of the SwiGLU values: bulk copies want 16-byte rows
 int lda(int I) { return (I + 7) / 8 * 8; }
 
@@ -282,6 +290,7 @@ size_t block_layout(int B, int E, int top_e, int I, int d, void* base, BlockArgs
                o_apx = take(B <= kExactTokens ? 0 : sizeof(float) * B * E), o_wn = take(sizeof(float) * E), o_ids = take(sizeof(int32_t) * P),
                o_w = take(sizeof(float) * P), o_off = take(sizeof(int32_t) * (E + 1)),
                o_rows = take(sizeof(int32_t) * P), o_a = take(sizeof(uint16_t) * P * lda(I)),
+               o_rest = take(two_terms(B, E, top_e) ? sizeof(uint16_t) * P * lda(I) : 0),
                o_out = take(sizeof(float) * P * d);
   if (base && a) {
     char* p = static_cast<char*>(base);
@@ -294,6 +303,7 @@ size_t block_layout(int B, int E, int top_e, int I, int d, void* base, BlockArgs
     a->offsets = reinterpret_cast<int32_t*>(p + o_off);
     a->rows = reinterpret_cast<int32_t*>(p + o_rows);
     a->a = reinterpret_cast<uint16_t*>(p + o_a);
+    a->a_rest = two_terms(B, E, top_e) ? reinterpret_cast<uint16_t*>(p + o_rest) : nullptr;
     a->out = reinterpret_cast<float*>(p + o_out);
     a->split = p + o_split;
   }
@@ -364,6 +374,7 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
   g.w = a.w_gate;
   g.w_up = a.w_up;
   g.y = a.a;
+  g.y_rest = a.a_rest;
   g.ldx = a.d;
   g.ldy = lda(a.I);
   g.err = a.err;
@@ -379,6 +390,7 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
   h.K = a.I;
   h.layout = 1;
   h.x = a.a;
+  h.x_rest = a.a_rest;
   h.x_div = 1;
   h.offsets = a.offsets;
   h.w = a.w_down;

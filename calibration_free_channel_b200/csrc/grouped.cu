@@ -78,6 +78,7 @@ enum Mode { kPlain, kSwiglu, kAdapter, kLowRank };
 
 struct Maps {
   CUtensorMap x[kRowBoxes], w, w_up;
+  CUtensorMap x_rest[kRowBoxes];  // x in two terms
   CUtensorMap z[kRowBoxes], z2, b;  // adapters (z2: 16 rows of both halves)
 };
 
@@ -89,11 +90,13 @@ struct TileArgs {
   int layout, gather, x_div, y_fp32;
   int max_split;
   int late_trigger;       // the next launch starts once everything before this one is complete
+  int two_terms;          // x is the sum of x and x_rest (in boxes)
   const uint16_t* x;
   const int32_t* x_rows;
   const int32_t* offsets;
   const int32_t* y_rows;
   void* y;
+  uint16_t* y_rest;       // kSwiglu: what the rounding of y leaves, or null
   uint32_t* err;
   uint32_t* count;        // [kMaxPairs][2] arrivals of a split tile's parts
   float* part;            // [kMaxPairs][2][cols / 4][128][4] the parts (four columns of a lane together)
@@ -441,6 +444,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   const Walk w = walk_of<kMode>(a, s);
   const int u0 = blockIdx.x >> 1, du = gridDim.x >> 1;
   volatile int* stop = &s.stop;
+  // x in two terms: the pair's first CTA holds the rows of the one, the second
+  // those of the other, and the accumulator has columns for both
+  const bool two = kMode == kPlain && a.two_terms;
 
   if (warp == 0 || (warp == 2 && !a.gather)) {
     // ----------------------- boxes: the weights (warp 0), the rows (warp 2).
@@ -468,7 +474,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     };
     for (int u = u0; u < w.units && ok; u += du) {
       const Tile t = tile_of<kMode>(a, s, w, u);
-      const int half = ((t.n + 31) & ~31) >> 1, c0 = (t.c0 * 2 + rank) * kChan, p = t.p0 + rank * half;
+      const int cols = (t.n + 31) & ~31, c0 = (t.c0 * 2 + rank) * kChan;
+      const int half = two ? cols : cols >> 1, p = two ? t.p0 : t.p0 + rank * half;  // this CTA's rows
       const uint32_t bytes = 2 * (kABytes + (a.gather ? 0 : half * 128));  // of both CTAs
       for (int kb = t.k0; kb < t.k1; kb++, it.next(a.stages), filled++) {
         const int k0 = kb * kBlockK;
@@ -477,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         uint8_t* A = ring + (size_t)it.st * a.stage_bytes;
         const uint32_t bar = full + it.st * 8;
         if (rows) {
-          fetch_rows(A + kABytes, maps.x, half,
+          fetch_rows(A + kABytes, two && rank ? maps.x_rest : maps.x, half,
                      [&](uint8_t* to, const CUtensorMap* m, int at) { tma_2d(to, m, k0, p + at, bar); });
           continue;
         }
@@ -534,7 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     for (int u = u0; u < w.units && ok; u += du, ti++) {
       const Tile t = tile_of<kMode>(a, s, w, u);
       const uint32_t d = tmem + (ti & 1) * kMaxCols;
-      const uint32_t idesc = mma_desc(2 * kLanes, (t.n + 31) & ~31, mn_a);
+      const uint32_t idesc = mma_desc(2 * kLanes, ((t.n + 31) & ~31) << (two ? 1 : 0), mn_a);
       ok = warp_wait(&s.acc_empty[ti & 1], ((ti >> 1) & 1) ^ 1, stop, a.err);
       if (!ok) break;
       tc_fence_after();
@@ -613,6 +620,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       if (bar_any(1, 128, !ok)) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q4 * 32) << 16) + (ti & 1) * kMaxCols;
+      auto load_columns = [&](int j0, float (&v)[32]) {
+        tmem_ld32(acc + j0, v);
+        if (two) {
+          float rest[32];
+          tmem_ld32(acc + ((t.n + 31) & ~31) + j0, rest);
+#pragma unroll
+          for (int j = 0; j < 32; j++) v[j] += rest[j];
+        }
+      };
       bool finish = true;
       const size_t part_size = (size_t)2 * a.cols * kLanes;
       float* part0 = a.part + (size_t)t.index * w.split * part_size + (size_t)rank * a.cols * kLanes + (q4 * 32 + lane) * 4;
@@ -620,7 +636,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         float* mine = part0 + t.part * part_size;
         for (int j0 = 0; j0 < t.n; j0 += 32) {
           float v[32];
-          tmem_ld32(acc + j0, v);
+          load_columns(j0, v);
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
             __stcg(reinterpret_cast<float4*>(mine + (j0 + j) * kLanes), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
@@ -645,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           else
             add_parts<kMaxSplit, 8>(part0 + j0 * kLanes, part_size, w.split, t.n - j0, v);
         } else {
-          tmem_ld32(acc + j0, v);
+          load_columns(j0, v);
         }
         if (kMode == kSwiglu) {
           // the gate side finishes the even columns, the up side the odd ones
@@ -681,6 +697,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
               const uint32_t p2 = odd ? bf16x2(o, r[i + 1]) : bf16x2(r[i], o);
               const int q = q_of[i + (odd ? 1 : 0)];
               st32_if(y + (size_t)q * a.ldy + c, p2, q >= 0 && in_n);
+              if (a.y_rest) {  // (an infinity leaves no rest)
+                const float lo = odd ? o : r[i], hi = odd ? r[i + 1] : o;
+                const float rl = isfinite(lo) ? lo - bf16lo(p2) : 0.0f, rh = isfinite(hi) ? hi - bf16hi(p2) : 0.0f;
+                st32_if(a.y_rest + (size_t)q * a.ldy + c, bf16x2(rl, rh), q >= 0 && in_n);
+              }
             }
           }
         } else if (kMode == kPlain && a.y_fp32) {
@@ -781,7 +802,7 @@ int most_cols(int n) { return n < kMaxCols ? (n + 31) / 32 * 32 : kMaxCols; }
 template <int kMode>
 cudaError_t run_tiles(const Maps& m, TileArgs t, cudaStream_t s) {
   // (32 at least: an adapter's narrowest columns with both halves of z)
-  t.b_rows = t.cols / 2 < 32 ? 32 : t.cols / 2;
+  t.b_rows = t.two_terms ? t.cols : t.cols / 2 < 32 ? 32 : t.cols / 2;
   t.stage_bytes = kABytes + t.b_rows * 128;
   t.stages = (kSmemBudget - (int)sizeof(Side)) / t.stage_bytes;
   if (t.stages > kMaxStages) t.stages = kMaxStages;
@@ -873,9 +894,13 @@ cudaError_t launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   t.count = static_cast<uint32_t*>(a.split);
   t.part = reinterpret_cast<float*>(static_cast<char*>(a.split) + align256(sizeof(uint32_t) * 2 * kMaxPairs));
   t.cols = choose_cols(a.P, a.G < a.P ? a.G : a.P, a.N, a.w_up ? kLanes : 2 * kLanes);
+  t.two_terms = a.x_rest != nullptr;
+  if (t.two_terms && t.cols > kMaxCols / 2) t.cols = kMaxCols / 2;  // both terms fit into a stage
+  t.y_rest = a.y_rest;
   Maps m;  // (what a mode does not use stays unset)
   const uint64_t N = a.N, K = a.K;
   bool ok = t.gather || row_maps(m.x, a.x, K, a.n_x, 0, 2ull * a.ldx, 0);
+  if (t.two_terms) ok = ok && row_maps(m.x_rest, a.x_rest, K, a.n_x, 0, 2ull * a.ldx, 0);
   if (a.w_up)
     ok = ok && tensor_map(&m.w, a.w, K, N, a.G, 2 * K, 2 * N * K, kBlockK, kLanes / 2) &&
          tensor_map(&m.w_up, a.w_up, K, N, a.G, 2 * K, 2 * N * K, kBlockK, kLanes / 2);

@@ -165,6 +165,7 @@ struct GroupedArgs {
   int ldx, ldy;             // row strides of x (a multiple of 8) and y, in elements
   int layout;               // 0: w [G, N, K]; 1: w [G, K, N]
   const uint16_t* x;        // [n_x, K]
+  const uint16_t* x_rest;   // or null: x + x_rest is multiplied (without x_rows)
   const int32_t* x_rows;    // [P] or null
   int x_div;
   const int32_t* offsets;   // [G + 1], or null: one group of all rows (G = 1)
@@ -172,6 +173,7 @@ struct GroupedArgs {
   const uint16_t* w_up;     // null: a plain product
   void* y;                  // [n_y, N] bf16, or fp32 with y_fp32
   int y_fp32;
+  uint16_t* y_rest;         // SwiGLU, even ldy: what the rounding of y leaves; or null
   const int32_t* y_rows;    // [P] or null
   int late_trigger;         // 1: the next launch may rely on all launches before this one
   uint32_t* err;
@@ -224,6 +226,7 @@ struct BlockArgs {
   int32_t* offsets;   // [E + 1]
   int32_t* rows;      // [B * top_e]
   uint16_t* a;        // [B * top_e, I rounded up to 8]
+  uint16_t* a_rest;   // the same, where the SwiGLU values are held in two terms
   float* out;         // [B * top_e, d]
   void* split;        // split_bytes(B * top_e)
 };

@@ -399,7 +399,8 @@ moe_status moe_reader_adapter_product(int T, int n_adapters, int N, int K, int r
  * routing rule of moe_reader_forward), groups the pairs by expert and runs
  * the two grouped products; the pairs' outputs are summed with their routing
  * weights in fp32, slot order, `residual` (may be NULL, may be y) added, one
- * rounding.  The SwiGLU values are rounded to bf16 between the products.
+ * rounding.  Between the products the SwiGLU values are held in two bf16
+ * terms (16 significant bits) while B top_e <= 64 E, and in one above.
  * ids: DEVICE [B, top_e] int32, receives the chosen experts; may be NULL.
  * Reads the router and the three weight matrices of the layer; expert_slot
  * must be NULL (MOE_EUNSUPPORTED otherwise). */
