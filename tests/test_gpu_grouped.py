@@ -415,6 +415,22 @@ def test_block_residual_in_place_and_repeatable():
     assert torch.equal(y, L.forward_grouped(x, res))
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** -20, 1.0, 2.0 ** 40, 2.0 ** 100])
+def test_block_outputs_of_any_size(scale):
+    # the pairs' outputs are held in 16 bits under a common exponent of 32 channels: no value over-
+    # or underflows, and a channel far below its neighbours keeps its bits
+    W = synth.layer_weights(synth.TINY, seed=26)
+    W["w_down"] = (W["w_down"].float() * scale).bfloat16()
+    W["w_down"][:, :, 5::32] *= 2.0 ** -20
+    L = M.Layer(W, top_e=2)
+    for B in (9, 700):
+        x = synth.tokens(256, B, seed=27).cuda()
+        y = L.forward_grouped(x)
+        L.check()
+        ref, _, tol = block_ref(x, L.w, 2)
+        close(y, ref, tol)
+
+
 def test_block_nan_token_stays_apart():
     W = synth.layer_weights(synth.TINY, seed=17)
     L = M.Layer(W, top_e=2)
