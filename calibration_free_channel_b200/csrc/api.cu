@@ -446,6 +446,7 @@ moe_status moe_reader_grouped_swiglu(int n_groups, int n_rows, int n_x, int I, i
   REQUIRE_PTR(w_gate);
   REQUIRE_PTR(w_up);
   REQUIRE_PTR(a);
+  REQUIRE(x != a, "a must not be x");
   st = check_workspace(workspace, ws_bytes, moe_reader_grouped_workspace_bytes(n_groups, n_rows));
   if (st != MOE_OK) return st;
   moe::GroupedArgs g = {};
@@ -487,6 +488,7 @@ moe_status moe_reader_grouped_product(int n_groups, int n_rows, int n_x, int n_y
   REQUIRE_PTR(offsets);
   REQUIRE_PTR(w);
   REQUIRE_PTR(y);
+  REQUIRE(x != y, "y must not be x");
   st = check_workspace(workspace, ws_bytes, moe_reader_grouped_workspace_bytes(n_groups, n_rows));
   if (st != MOE_OK) return st;
   moe::GroupedArgs g = {};

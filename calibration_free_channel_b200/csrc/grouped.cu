@@ -114,12 +114,18 @@ struct Side {
   int stop, tiles, last;
   unsigned long long scan[kGThreads / 32];
   alignas(16) int y_row[kMaxCols];  // result row of each column, -1: none; even columns, then odd ones
-  float swap[2][2][2][16][32];      // [quarter][turn][from the up side][column][lane]
   int first[kMaxGroups];            // first sorted position of each group
   int rows[kMaxGroups];             // rows of each group
   int before[kMaxGroups];           // row tiles of the groups before (adapters: rows of z before)
   int z_before[kMaxGroups];         // kLowRank: rows of z before
+  float swap[2][2][2][16][32];      // kSwiglu: [quarter][turn][from the up side][column][lane]
 };
+
+// What a mode's launch has of it (swap is last).
+template <int kMode>
+constexpr int side_bytes() {
+  return (int)sizeof(Side) - (kMode == kSwiglu ? 0 : (int)sizeof(float) * 2 * 2 * 2 * 16 * 32);
+}
 
 // A role's place in the ring: the stage, and how often it has gone round.
 struct Turn {
@@ -146,7 +152,7 @@ __device__ void lay_tiles(const TileArgs& a, Side& s) {
     const int g = tid * kPer + i;
     t[i] = z[i] = 0;
     if (g < a.G) {
-      const int p0 = a.offsets ? a.offsets[g] : 0, p1 = a.offsets ? a.offsets[g + 1] : a.P;
+      const int p0 = a.offsets ? __ldcg(a.offsets + g) : 0, p1 = a.offsets ? __ldcg(a.offsets + g + 1) : a.P;
       const bool fine = p0 >= 0 && p1 >= p0 && p1 <= a.P;
       bad |= !fine;
       if (fine && kZ) z[i] = padded_rows(p0, p1);
@@ -310,7 +316,7 @@ __device__ void gather_rows(const TileArgs& a, Side& s, uint8_t* ring, const Wal
       // stored, or as zeros)
       int row = 0;
       if (r0 + 16 * m < half) {
-        row = a.x_rows[min(tl.p0 + min(rank * half + r0 + 16 * m, tl.n - 1), a.P - 1)];
+        row = __ldcg(a.x_rows + min(tl.p0 + min(rank * half + r0 + 16 * m, tl.n - 1), a.P - 1));
         row = row < 0 ? -1 : row / a.x_div;
         if (row < 0 || row >= a.n_x) {
           atomicOr(a.err, kErrBadPlan);
@@ -429,7 +435,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   }
   if (warp == 2) tmem_alloc(&s.tmem, 512);
   // Adapters: the launch before this one, of z, lets it start only once
-  // everything earlier has completed, so only z is waited for.
+  // everything earlier has completed, so only z is waited for.  (The plan, x
+  // and base are read through L2, not through an L1 that was filled earlier.)
   if (kMode != kAdapter) {
     if (!a.late_trigger) pdl_trigger();
     pdl_wait();
@@ -599,18 +606,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           const int p = t.p0 + j;
           if (j < t.n) {
             q = s.z_before[t.g] + p - s.first[t.g];
-            const bool own = p >= a.offsets[t.g] && p < a.offsets[t.g + 1];
-            const int row = own ? a.x_rows[p] : -1;
+            const bool own = p >= __ldcg(a.offsets + t.g) && p < __ldcg(a.offsets + t.g + 1);
+            const int row = own ? __ldcg(a.x_rows + p) : -1;
             if (row < 0 || row >= a.n_x) q = -2 - q;
           }
         } else if (j < t.n) {
-          q = a.y_rows ? a.y_rows[t.p0 + j] : t.p0 + j;
+          q = a.y_rows ? __ldcg(a.y_rows + t.p0 + j) : t.p0 + j;
           if (q < 0 || q >= a.n_y) {
             atomicOr(a.err, kErrBadPlan);
             q = -1;
           }
           if (a.gather) {  // a row that is not there has no result
-            const int row = a.x_rows[t.p0 + j];
+            const int row = __ldcg(a.x_rows + t.p0 + j);
             if (row < 0 || row / a.x_div >= a.n_x) q = -1;
           }
         }
@@ -804,10 +811,13 @@ cudaError_t run_tiles(const Maps& m, TileArgs t, cudaStream_t s) {
   // (32 at least: an adapter's narrowest columns with both halves of z)
   t.b_rows = t.two_terms ? t.cols : t.cols / 2 < 32 ? 32 : t.cols / 2;
   t.stage_bytes = kABytes + t.b_rows * 128;
-  t.stages = (kSmemBudget - (int)sizeof(Side)) / t.stage_bytes;
+  // Beside the launch of z for few tokens, whose CTAs take up to 73 KB, a pair
+  // finds room only if it takes the rest at most; it starts 5 us later otherwise.
+  const int budget = kMode == kAdapter && t.P <= kFewTokens ? kSmemBudget - 74 * 1024 : kSmemBudget;
+  t.stages = (budget - side_bytes<kMode>()) / t.stage_bytes;
   if (t.stages > kMaxStages) t.stages = kMaxStages;
   t.max_split = kMode == kLowRank ? 1 : kMaxSplit;
-  const size_t smem = 1024 + (size_t)t.stages * t.stage_bytes + sizeof(Side);
+  const size_t smem = 1024 + (size_t)t.stages * t.stage_bytes + side_bytes<kMode>();
   DeviceState* dev = nullptr;
   cudaError_t e = device_state(&dev);
   if (e == cudaSuccess && !dev->allowed[kMode]) {

@@ -126,7 +126,7 @@ __device__ __forceinline__ void st16_if(void* p, uint16_t v, bool on) {
 }
 __device__ __forceinline__ uint32_t ld32_if(const void* p, bool on) {
   uint32_t v;
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n mov.b32 %0, 0;\n @p ld.global.b32 %0, [%1];\n}"
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n mov.b32 %0, 0;\n @p ld.global.cg.b32 %0, [%1];\n}"
                : "=r"(v)
                : "l"(p), "r"((uint32_t)on)
                : "memory");

@@ -446,7 +446,8 @@ class Layer:
         if self._wsg is None or self._wsg.numel() < nb:
             self._wsg = torch.zeros(max(nb, 16), dtype=torch.uint8, device=x.device)
         y = out if out is not None else torch.empty_like(x)
-        moe_reader_forward_grouped(self.struct(0), B, x, residual, y, ids, self._wsg, self._wsg.numel(), stream)
+        with torch.cuda.device(x.device):
+            moe_reader_forward_grouped(self.struct(0), B, x, residual, y, ids, self._wsg, self._wsg.numel(), stream)
         return y
 
     def check(self, stream=None):

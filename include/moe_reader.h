@@ -322,9 +322,12 @@ moe_status moe_reader_forward_noalloc(const moe_reader_layer* layer, int B, int 
  *    offsets[n_groups] on belong to no group: their outputs are left as
  *    they were.
  *  - Widths (N, K, d) are multiples of 8 in [8, 32768] and bf16 rows are dense.
+ *  - Pointers belong to the current device; outputs and workspace overlap no
+ *    input (base and residual may be y itself).
  *  - Products are exact, sums fp32 over the whole length of K, one rounding to
- *    bf16 at the end.  A row's output does not depend on the other rows.
- *    Results are the same bits from call to call on the same plan.
+ *    bf16 at the end.  What a row holds reaches no other row's output, NaN
+ *    and infinities included.  Results are the same bits from call to call
+ *    on the same plan.
  *  - Plans are checked on the device where they are read: an offset outside
  *    [0, n_rows] or below the one before it, or a row index outside its
  *    matrix, records device error bit 8 (moe_reader_check_error:

@@ -522,6 +522,83 @@ def test_captured_block_replays_on_new_inputs():
     L.check()
 
 
+@pytest.mark.parametrize("T", [3, 90, 900])
+def test_captured_plan_and_adapters_replay_on_new_inputs(T):
+    """Ids, plan and adapters in one graph: each replay uses the ids and tokens
+    that the graph's own first kernels put there."""
+    A, K, N, r = 6, 256, 520, 24
+    x, w, base = dev(T, K, seed=80), dev(N, K, seed=81, scale=K ** -0.5), dev(T, N, seed=82)
+    a, b = dev(A, r, K, seed=83, scale=K ** -0.5), dev(A, N, r, seed=84)
+    new_x, new_ids = x.clone(), ids_of(T, A, "random")
+    ids = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    off, rows = torch.zeros(A + 1, dtype=torch.int32, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    ws = ws_for(M.moe_reader_adapter_workspace_bytes(T, A, K, N, r))
+
+    def step():
+        ids.copy_(new_ids)
+        x.copy_(new_x)
+        M.moe_reader_group_rows(T, A, ids, off, rows, ws, ws.numel())
+        M.moe_reader_adapter_product(T, A, N, K, r, x, w, base, off, rows, a, b, None, y, ws, ws.numel())
+
+    step()
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        step()
+    for k in range(4):
+        new_ids.copy_(ids_of(T, A, ("random", "none", "runs", "all")[k], seed=k))
+        new_x.copy_(dev(T, K, seed=90 + k))
+        g.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(got, y)
+        xd, idc = new_x.double(), new_ids
+        ref = xd @ w.double().T + base.double()
+        err = sum_err(K) * (xd.abs() @ w.double().abs().T)
+        for q in range(A):
+            t = (idc == q).nonzero().flatten()
+            z = xd[t] @ a[q].double().T
+            mag = xd[t].abs() @ a[q].double().abs().T
+            ref[t] += z @ b[q].double().T
+            err[t] += (sum_err(K) * mag + 2.0 ** -15 * z.abs()) @ b[q].double().abs().T
+        close(got, ref, HALF * ref.abs() + SLACK * err + 2.0 ** -20 * (ref.abs() + base.double().abs()))
+    M.moe_reader_check_error(ws)
+
+
+def test_one_workspace_serves_every_entry_point_in_turn():
+    """The counters that split sums use sit at one place for all: a workspace
+    goes from one entry point and size to the next."""
+    T, A, K, N, r, E = 70, 4, 2048, 512, 16, 4
+    big = max(M.moe_reader_block_workspace_bytes(300, 8, 2, 128, 256), M.moe_reader_grouped_workspace_bytes(E, 600),
+              M.moe_reader_adapter_workspace_bytes(T, A, K, N, r))
+    shared = ws_for(big)
+    W = {k: v.cuda() if v is not None else None for k, v in synth.layer_weights(synth.TINY, seed=28).items()}
+    st = M.Layer(W, top_e=2).struct(0)
+    x, w, xb = dev(600, K, seed=85), dev(E, N, K, seed=86), synth.tokens(256, 300, seed=29).cuda()
+    a, b = dev(A, r, K, seed=87, scale=K ** -0.5), dev(A, N, r, seed=88)
+    off1, rows1, _ = plan_of([3, 0, 40, 27], 1)
+
+    def run(ws_of):
+        outs = []
+        for n in (5, 300, 40):  # few tokens and many, so that sums are split and not
+            y = torch.empty((n, 256), dtype=torch.bfloat16, device="cuda")
+            M.moe_reader_forward_grouped(st, n, xb, None, y, None, ws_of(), big)
+            outs.append(y)
+            p = torch.empty((70, N), dtype=torch.bfloat16, device="cuda")
+            M.moe_reader_grouped_product(E, 70, 600, 70, N, K, 0, x, None, 1, off1, w, p, None, ws_of(), big)
+            outs.append(p)
+            z = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+            M.moe_reader_adapter_product(T, A, N, K, r, x, w[0], None, off1, rows1, a, b, None, z, ws_of(), big)
+            outs.append(z)
+        return outs
+
+    for u, v in zip(run(lambda: shared), run(lambda: ws_for(big))):
+        assert torch.equal(u, v)
+    M.moe_reader_check_error(shared)
+
+
 def test_two_streams_with_their_own_workspaces():
     W = synth.layer_weights(synth.BlockShape(16, 256, 1024, 4), seed=24, device="cuda")
     layers = [M.Layer(W, top_e=4) for _ in range(2)]

@@ -25,10 +25,10 @@ def call(lib, name, order, defaults, **kw):
 GROUP = ("n n_groups ids offsets rows ws nb stream".split(),
          dict(n=64, n_groups=8, ids=F, offsets=F, rows=F, ws=F, nb=BIG, stream=None))
 SWIGLU = ("G P n_x I d x x_rows x_div offsets wg wu a ws nb stream".split(),
-          dict(G=8, P=64, n_x=32, I=128, d=256, x=F, x_rows=F, x_div=2, offsets=F, wg=F, wu=F, a=F, ws=F, nb=BIG,
+          dict(G=8, P=64, n_x=32, I=128, d=256, x=F, x_rows=F, x_div=2, offsets=F, wg=F, wu=F, a=0x20000, ws=F, nb=BIG,
                stream=None))
 PRODUCT = ("G P n_x n_y N K layout x x_rows x_div offsets w y y_rows ws nb stream".split(),
-           dict(G=8, P=64, n_x=64, n_y=64, N=128, K=256, layout=0, x=F, x_rows=None, x_div=1, offsets=F, w=F, y=F,
+           dict(G=8, P=64, n_x=64, n_y=64, N=128, K=256, layout=0, x=F, x_rows=None, x_div=1, offsets=F, w=F, y=0x20000,
                 y_rows=None, ws=F, nb=BIG, stream=None))
 ADAPTER = ("T A N K r x w base offsets rows a b scale y ws nb stream".split(),
            dict(T=64, A=8, N=128, K=256, r=16, x=F, w=F, base=None, offsets=F, rows=F, a=F, b=F, scale=None,
@@ -47,7 +47,7 @@ def test_group_rows_refuses(lib, kw):
     dict(G=0), dict(G=2000), dict(P=0), dict(P=-1), dict(P=(1 << 20) + 1), dict(n_x=0), dict(n_x=(1 << 20) + 1),
     dict(I=0), dict(I=32769), dict(d=0), dict(d=252), dict(d=32776), dict(x=None), dict(x=F + 2),
     dict(x_rows=None), dict(x_rows=None, x_div=1), dict(x_rows=F + 4), dict(x_div=0), dict(offsets=None),
-    dict(wg=None), dict(wu=None), dict(wu=F + 8), dict(a=None), dict(a=F + 2), dict(ws=None), dict(nb=16)])
+    dict(wg=None), dict(wu=None), dict(wu=F + 8), dict(a=None), dict(a=F + 2), dict(a=F), dict(ws=None), dict(nb=16)])
 def test_grouped_swiglu_refuses(lib, kw):
     assert call(lib, "moe_reader_grouped_swiglu", *SWIGLU, **kw) == M.MOE_EINVAL
     assert lib.moe_reader_last_error()
@@ -56,7 +56,7 @@ def test_grouped_swiglu_refuses(lib, kw):
 @pytest.mark.parametrize("kw", [
     dict(G=0), dict(P=0), dict(n_x=63), dict(n_y=63), dict(n_y=0), dict(n_y=(1 << 20) + 1), dict(N=0), dict(N=12),
     dict(N=32776), dict(K=4), dict(K=260), dict(layout=2), dict(layout=-1), dict(x=None), dict(x_div=2),
-    dict(offsets=F + 4), dict(w=None), dict(w=F + 8), dict(y=None), dict(y_rows=F + 4), dict(ws=None), dict(nb=0)])
+    dict(offsets=F + 4), dict(w=None), dict(w=F + 8), dict(y=None), dict(y=F), dict(y_rows=F + 4), dict(ws=None), dict(nb=0)])
 def test_grouped_product_refuses(lib, kw):
     assert call(lib, "moe_reader_grouped_product", *PRODUCT, **kw) == M.MOE_EINVAL
     assert lib.moe_reader_last_error()
