@@ -8,7 +8,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kExactTokens = 32;  // up to here every logit is summed in fp64
+// Up to here every logit is summed in fp64 (whole Qwen-sized block: 32 tokens
+// 210 us against 229 by the tensor cores' logits, 64 248 against 253, 128 258
+// against 256).
+constexpr int kExactTokens = 64;
 
 // Routing.  The rule is fp64: logits of exact products summed in 64 bits, the
 // largest top_e, ties to the lower id, slot 0 the largest.  Up to kExactTokens
@@ -265,8 +268,9 @@ __global__ void __launch_bounds__(256) combine_kernel(BlockArgs a) {
 // to the result as its own rounding does.  While an expert has 64 tokens or
 // fewer on average they are held in two bf16 terms, 16 significant bits: the
 // second product is bound by its weights there, and the second term's rows and
-// products cost nothing that shows.  Above that they would: half of the
-// block's products again.
+// products cost 2 % of the whole (1024 tokens, 128 experts, top-8: 301 against
+// 295 us).  Above that they cost more: 9 % at 2048 tokens, in the end half of
+// the products again.
 bool two_terms(int B, int E, int top_e) { return (long)B * top_e <= 64L * E; }
 
 // row stride of the SwiGLU values: bulk copies want 16-byte rows

@@ -32,6 +32,15 @@
 //
 // A call with few tiles splits their sums over K: each part is written in
 // fp32, and the CTA that arrives last adds them in order and finishes the tile.
+//
+// What bounds it: few rows a group, the weights' bytes (128 experts of 768 x
+// 2048, gate and up, 4 rows each: 134 us, 6.0 TB/s); many, the stages' way
+// through a ring that holds 192 KB a CTA (512 rows each: 345 us, 1190 TFLOP/s,
+// as much as a batched library product of the same shape; 380 us gathered),
+// and in a row of calls the power limit (about 1.0 GHz at 990 W).  Copies of
+// the weights into L2 ahead of the ring made every size slower, since they
+// cost the copy engine as much as the copies themselves; so did tiles sorted by
+// size, for few rows by more than the better balance gave for many.
 #include <cudaTypedefs.h>
 
 #include "kernels.h"
@@ -69,8 +78,13 @@ constexpr int kABytes = kLanes * kBlockK * 2;
 constexpr int kMaxStages = 8;
 constexpr int kMaxPairs = 74;              // CTA pairs of a launch
 constexpr int kMaxSplit = 8;               // parts of a tile's sum
-constexpr int kFewTokens = 512;            // up to here z comes from adapter.cu
-constexpr int kMinPart = 8;                // stages of K that a part has at least
+// Up to here z comes from adapter.cu (8 adapters, rank 64, 2048 x 2048, whole
+// call: 512 tokens 29.7 us against 37.0 with z's tiles, 2048 42.7 against
+// 44.7; 4100 tokens beside 4096 channels 119 against 101).
+constexpr int kFewTokens = 2048;
+// Stages of K that a part has at least (one token, 2048 x 2048: 12.8 us at 8,
+// 13.2 at 4, 17.8 without parts; K = 512: 10.3 without, 11.1 with two).
+constexpr int kMinPart = 8;
 constexpr int kRowBoxes = 4;               // boxes of 128, 64, 32 and 16 rows
 constexpr int kSmemBudget = 227 * 1024 - 1024;  // 1024: the ring's alignment
 
