@@ -115,6 +115,33 @@ def test_grouped_product_sizes(layout, sizes):
     close(*run_product(dev(sum(sizes), K, seed=4), w, sizes, layout, False, True))
 
 
+@pytest.mark.parametrize("sizes", [[257, 0, 900, 3, 512], [2000, 512, 511, 513, 290, 1, 300], [640] * 9 + [7, 33, 256]])
+@pytest.mark.parametrize("kind", ["layout 0", "layout 1", "gathered"])
+def test_grouped_product_large_groups(sizes, kind):
+    # groups of hundreds of rows, several tiles each, between small ones
+    K, N, G = 392, 1032, len(sizes)
+    layout = int(kind == "layout 1")
+    w = dev(G, K, N, seed=18) if layout else dev(G, N, K, seed=18)
+    close(*run_product(dev(sum(sizes), K, seed=19), w, sizes, layout, kind == "gathered", True))
+
+
+@pytest.mark.parametrize("gather", [True, False])
+def test_grouped_swiglu_large_groups(gather):
+    sizes, I, d = [700, 2, 0, 290, 1500, 256], 200, 264
+    off, rows, P = plan_of(sizes, 4)
+    x, wg, wu = dev(P, d, seed=24), dev(6, I, d, seed=25, scale=2 * d ** -0.5), dev(6, I, d, seed=26)
+    a = torch.empty((P, I), dtype=torch.bfloat16, device="cuda")
+    ws = ws_for(M.moe_reader_grouped_workspace_bytes(6, P))
+    M.moe_reader_grouped_swiglu(6, P, P, I, d, x, rows if gather else None, 1, off, wg, wu, a, ws, ws.numel())
+    M.moe_reader_check_error(ws)
+    o = off.tolist()
+    for g in range(6):
+        p = torch.arange(o[g], o[g + 1], device="cuda")
+        if p.numel():
+            ref, e = swiglu_ref(x[rows[p].long() if gather else p], wg[g], wu[g])
+            close(a[p], ref, HALF * ref.abs() + SLACK * e)
+
+
 def test_grouped_product_no_rows():
     # every group empty: nothing is written
     y, ref, tol = run_product(dev(64, 64, seed=5), dev(3, 64, 64, seed=6), [0, 0, 0], 0, False, False, extra=40)
