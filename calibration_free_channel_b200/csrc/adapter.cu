@@ -11,6 +11,9 @@
 // 64 tokens of 32 adapters, rank 32, K = 2048: 6 us, four of them waiting for
 // loads that each touch eight rows.
 //
+// (Loads here and in block.cu are plain ones: a launch that starts before its
+// predecessor's end may not read what that wrote through the read-only path.)
+//
 // z is held as two bf16 terms, the rounded value and what the rounding left,
 // 16 significant bits together: rounding it to one would add as much error as
 // the rounding of the result.  Rows of z that a 32-row step of the tiles
@@ -119,13 +122,13 @@ __global__ void __launch_bounds__(512) z_kernel(AdapterArgs a, size_t z_rows) {
       for (int k0 = kw * 32; k0 < a.K; k0 += 32 * kKWarps) {
         const int k = k0 + t4 * 8;
         const bool in = k < a.K;
-        uint4 x0 = in && xr[0] ? __ldg(reinterpret_cast<const uint4*>(xr[0] + k)) : zero;
-        uint4 x1 = in && xr[1] ? __ldg(reinterpret_cast<const uint4*>(xr[1] + k)) : zero;
+        uint4 x0 = in && xr[0] ? *reinterpret_cast<const uint4*>(xr[0] + k) : zero;
+        uint4 x1 = in && xr[1] ? *reinterpret_cast<const uint4*>(xr[1] + k) : zero;
         uint4 b[kNT];
 #pragma unroll
         for (int i = 0; i < kNT; i++) {
           const int j = j0 + i * 8 + gr;
-          b[i] = in && j < r ? __ldg(reinterpret_cast<const uint4*>(A + (size_t)j * a.K + k)) : zero;
+          b[i] = in && j < r ? *reinterpret_cast<const uint4*>(A + (size_t)j * a.K + k) : zero;
         }
 #pragma unroll
         for (int i = 0; i < kNT; i++) {

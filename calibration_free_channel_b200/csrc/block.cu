@@ -3,6 +3,7 @@
 // the weighted sum of a token's pairs.
 #include "common.cuh"
 #include "kernels.h"
+#include "sort.cuh"
 
 namespace moe {
 
@@ -29,8 +30,8 @@ __device__ __forceinline__ void dot64x2(const uint16_t* x, const uint16_t* w0, c
   s0 = s1 = 0.0;
 #pragma unroll 4
   for (int k = lane * 8; k < d; k += 256) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k)), b = __ldg(reinterpret_cast<const uint4*>(w0 + k)),
-                c = __ldg(reinterpret_cast<const uint4*>(w1 + k));
+    const uint4 a = *reinterpret_cast<const uint4*>(x + k), b = *reinterpret_cast<const uint4*>(w0 + k),
+                c = *reinterpret_cast<const uint4*>(w1 + k);
     const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w}, cv[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
     for (int i = 0; i < 4; i++) {  // products of two bf16 are exact in fp32
@@ -54,7 +55,7 @@ __device__ __forceinline__ float norm2(const uint16_t* x, int d, int lane) {
   float s = 0.0f;
 #pragma unroll 4
   for (int k = lane * 8; k < d; k += 256) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k));
+    const uint4 a = *reinterpret_cast<const uint4*>(x + k);
     const uint32_t av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -118,6 +119,38 @@ __device__ __forceinline__ void largest(const V (&v)[kM], int E, int lane, uint3
   if ((id & 31) == lane && id != 0x7fffffff) taken |= 1u << (id >> 5);
 }
 
+// The choice by fp64 logits, one warp; E <= 32 kM.
+template <int kM>
+__device__ __forceinline__ void choose_exact(const BlockArgs& a, int t, int lane) {
+  uint32_t taken = 0;
+  int id = 0;
+  double v[kM], mine = 0.0;
+#pragma unroll
+  for (int m = 0; m < kM; m++) v[m] = lane + 32 * m < a.E ? ranked(a.logits[(size_t)t * a.E + lane + 32 * m]) : 0.0;
+  for (int s = 0; s < a.top_e; s++) {
+    double best;
+    int e;
+    largest(v, a.E, lane, taken, best, e);
+    if (lane == s) {
+      mine = best;
+      id = e;
+    }
+  }
+  put_choice(a, t, lane < a.top_e ? lane : -1, id, mine);
+}
+
+// Few tokens and experts: the choice and the plan of its pairs in one CTA,
+// one launch less (of about 4 us each) in the chain of a small block.
+__global__ void __launch_bounds__(1024) choose_and_group_kernel(BlockArgs a, int bits, int stretch) {
+  extern __shared__ uint8_t raw[];
+  pdl_trigger();
+  sort_rows(a.B * a.top_e, a.E, bits, stretch, a.ids, a.offsets, a.rows, raw, [&] {
+    pdl_wait();
+    for (int t = threadIdx.x >> 5; t < a.B; t += 32) choose_exact<4>(a, t, threadIdx.x & 31);
+    __syncthreads();  // (the ids, written through global memory by this CTA)
+  });
+}
+
 // The logits of two experts for token x, in fp64.
 __device__ __forceinline__ void exact_logits(const BlockArgs& a, const uint16_t* x, int e0, int e1, int lane,
                                              double& l0, double& l1) {
@@ -136,20 +169,7 @@ __global__ void __launch_bounds__(256) choose_kernel(BlockArgs a) {
   uint32_t taken = 0;
   int id = 0;
   if (kExact) {
-    double v[kM], mine = 0.0;
-#pragma unroll
-    for (int m = 0; m < kM; m++)
-      v[m] = lane + 32 * m < a.E ? ranked(a.logits[(size_t)t * a.E + lane + 32 * m]) : 0.0;
-    for (int s = 0; s < a.top_e; s++) {
-      double best;
-      int e;
-      largest(v, a.E, lane, taken, best, e);
-      if (lane == s) {
-        mine = best;
-        id = e;
-      }
-    }
-    put_choice(a, t, lane < a.top_e ? lane : -1, id, mine);
+    choose_exact<kM>(a, t, lane);
     return;
   }
   const uint16_t* x = a.x + (size_t)t * a.d;
@@ -329,6 +349,7 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kernel, a);
   };
   const int by8 = (a.B + 7) / 8;
+  bool grouped = false;
   cudaError_t e;
   if (a.B <= kExactTokens) {
     RouteArgs r = {};
@@ -340,8 +361,17 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
     r.bias = a.bias;
     r.ws.logits = a.logits;
     e = launch_logits(r, s);
-    if (e == cudaSuccess)
-      e = a.E <= 128 ? launch(choose_kernel<4, true>, by8) : launch(choose_kernel<32, true>, by8);
+    if (e == cudaSuccess && a.E <= 128) {
+      const int stretch = sort_stretch(P, 1);
+      cudaLaunchConfig_t one = cfg;
+      one.gridDim = dim3(1);
+      one.blockDim = dim3(1024);
+      one.dynamicSmemBytes = sort_bytes(P, a.E, stretch);  // (32 warps' tables of 129 counts at most)
+      e = cudaLaunchKernelEx(&one, choose_and_group_kernel, a, sort_bits(a.E), stretch);
+      grouped = true;
+    } else if (e == cudaSuccess) {
+      e = launch(choose_kernel<32, true>, by8);
+    }
   } else {
     GroupedArgs l = {};
     l.G = 1;
@@ -361,8 +391,7 @@ cudaError_t launch_block(const BlockArgs& a, cudaStream_t s) {
     if (e == cudaSuccess)
       e = a.E <= 128 ? launch(choose_kernel<4, false>, by8) : launch(choose_kernel<32, false>, by8);
   }
-  if (e != cudaSuccess) return e;
-  e = launch_group_rows(P, a.E, a.ids, a.offsets, a.rows, s);
+  if (e == cudaSuccess && !grouped) e = launch_group_rows(P, a.E, a.ids, a.offsets, a.rows, s);
   if (e != cudaSuccess) return e;
   GroupedArgs g = {};
   g.G = a.E;
