@@ -121,11 +121,29 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _ptrs(*args):
+    """Pointers of the grouped entry points' arrays: tensors have to be
+    contiguous and on the current device (a strided, host or other device's
+    tensor would have the kernels read memory that is not its values)."""
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
+    out = []
+    for t in args:
+        if t is None or type(t) is int:
+            out.append(t)
+        elif t.get_device() == dev and t.is_contiguous():
+            out.append(t.data_ptr())
+        elif t.get_device() != dev:
+            raise MoeError(MOE_EINVAL, f"a tensor is on {t.device}, not on the current CUDA device")
+        else:
+            raise MoeError(MOE_EINVAL, f"a tensor of shape {tuple(t.shape)} is not contiguous")
+    return out
+
+
 def _stream(stream):
     if stream is None:
         # the current stream's handle without building a Stream object (which costs more than a launch);
         # before torch has set CUDA up, that is the default stream
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if torch.cuda.is_initialized() else None
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if torch.cuda.is_initialized() else None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -198,8 +216,7 @@ def moe_reader_group_workspace_bytes(n, n_groups) -> int:
 
 
 def moe_reader_group_rows(n, n_groups, ids, offsets, rows, workspace, ws_bytes, stream=None):
-    _check(lib().moe_reader_group_rows(n, n_groups, _ptr(ids), _ptr(offsets), _ptr(rows), _ptr(workspace), ws_bytes,
-                                       _stream(stream)))
+    _check(lib().moe_reader_group_rows(n, n_groups, *_ptrs(ids, offsets, rows, workspace), ws_bytes, _stream(stream)))
 
 
 def moe_reader_grouped_workspace_bytes(n_groups, n_rows) -> int:
@@ -208,16 +225,16 @@ def moe_reader_grouped_workspace_bytes(n_groups, n_rows) -> int:
 
 def moe_reader_grouped_swiglu(n_groups, n_rows, n_x, I, d, x, x_rows, x_div, offsets, w_gate, w_up, a, workspace,
                               ws_bytes, stream=None):
-    _check(lib().moe_reader_grouped_swiglu(n_groups, n_rows, n_x, I, d, _ptr(x), _ptr(x_rows), x_div, _ptr(offsets),
-                                           _ptr(w_gate), _ptr(w_up), _ptr(a), _ptr(workspace), ws_bytes,
+    x, x_rows, *rest = _ptrs(x, x_rows, offsets, w_gate, w_up, a, workspace)
+    _check(lib().moe_reader_grouped_swiglu(n_groups, n_rows, n_x, I, d, x, x_rows, x_div, *rest, ws_bytes,
                                            _stream(stream)))
 
 
 def moe_reader_grouped_product(n_groups, n_rows, n_x, n_y, N, K, w_layout, x, x_rows, x_div, offsets, w, y, y_rows,
                                workspace, ws_bytes, stream=None):
-    _check(lib().moe_reader_grouped_product(n_groups, n_rows, n_x, n_y, N, K, w_layout, _ptr(x), _ptr(x_rows), x_div,
-                                            _ptr(offsets), _ptr(w), _ptr(y), _ptr(y_rows), _ptr(workspace), ws_bytes,
-                                            _stream(stream)))
+    x, x_rows, *rest = _ptrs(x, x_rows, offsets, w, y, y_rows, workspace)
+    _check(lib().moe_reader_grouped_product(n_groups, n_rows, n_x, n_y, N, K, w_layout, x, x_rows, x_div, *rest,
+                                            ws_bytes, _stream(stream)))
 
 
 def moe_reader_adapter_workspace_bytes(T, n_adapters, K, N, r) -> int:
@@ -226,9 +243,9 @@ def moe_reader_adapter_workspace_bytes(T, n_adapters, K, N, r) -> int:
 
 def moe_reader_adapter_product(T, n_adapters, N, K, r, x, w, base, offsets, rows, a, b, scale, y, workspace, ws_bytes,
                                stream=None):
-    _check(lib().moe_reader_adapter_product(T, n_adapters, N, K, r, _ptr(x), _ptr(w), _ptr(base), _ptr(offsets),
-                                            _ptr(rows), _ptr(a), _ptr(b), _ptr(scale), _ptr(y), _ptr(workspace),
-                                            ws_bytes, _stream(stream)))
+    _check(lib().moe_reader_adapter_product(T, n_adapters, N, K, r,
+                                            *_ptrs(x, w, base, offsets, rows, a, b, scale, y, workspace), ws_bytes,
+                                            _stream(stream)))
 
 
 def moe_reader_block_workspace_bytes(B, E, top_e, I, d) -> int:
@@ -236,8 +253,8 @@ def moe_reader_block_workspace_bytes(B, E, top_e, I, d) -> int:
 
 
 def moe_reader_forward_grouped(layer: MoeReaderLayer, B, x, residual, y, ids, workspace, ws_bytes, stream=None):
-    _check(lib().moe_reader_forward_grouped(C.byref(layer), B, _ptr(x), _ptr(residual), _ptr(y), _ptr(ids),
-                                            _ptr(workspace), ws_bytes, _stream(stream)))
+    _check(lib().moe_reader_forward_grouped(C.byref(layer), B, *_ptrs(x, residual, y, ids, workspace), ws_bytes,
+                                            _stream(stream)))
 
 
 def moe_reader_rmsnorm(B, d, eps, x, h, stream=None):

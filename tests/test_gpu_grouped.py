@@ -527,6 +527,15 @@ def test_bad_adapter_rows_are_reported():
         M.moe_reader_check_error(ws)
 
 
+def test_strided_tensors_are_refused_by_the_binding():
+    ids = torch.zeros(128, dtype=torch.int32, device="cuda")
+    off, rows = torch.zeros(9, dtype=torch.int32, device="cuda"), torch.zeros(64, dtype=torch.int32, device="cuda")
+    ws = ws_for(M.moe_reader_group_workspace_bytes(64, 8))
+    for bad in (ids[::2], ids[:1].expand(64)):
+        with pytest.raises(M.MoeError, match="MOE_EINVAL.*contiguous"):
+            M.moe_reader_group_rows(64, 8, bad, off, rows, ws, ws.numel())
+
+
 # ------------------------------------------- streams, graphs, used together
 def test_captured_block_replays_on_new_inputs():
     W = synth.layer_weights(synth.TINY, seed=20)

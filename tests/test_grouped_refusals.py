@@ -3,6 +3,7 @@ is enqueued (no GPU needed)."""
 import ctypes as C
 
 import pytest
+import torch
 
 from calibration_free_channel_b200 import build as Bld
 from calibration_free_channel_b200 import moe_reader as M
@@ -94,6 +95,14 @@ def test_forward_grouped_refuses(lib, kw, args):
 def test_forward_grouped_refuses_compacted_shards(lib):
     assert _block(lib, _layer(expert_slot=F)) == M.MOE_EUNSUPPORTED
     assert b"expert_slot" in lib.moe_reader_last_error()
+
+
+def test_host_tensors_are_refused_by_the_binding():
+    t = torch.zeros(64, dtype=torch.int32)
+    with pytest.raises(M.MoeError, match="MOE_EINVAL.*cpu"):
+        M.moe_reader_group_rows(64, 8, t, F, F, F, BIG)
+    with pytest.raises(M.MoeError, match="MOE_EINVAL.*cpu"):
+        M.moe_reader_forward_grouped(_layer(), 300, t, None, F, None, F, BIG)
 
 
 def test_workspace_queries(lib):
