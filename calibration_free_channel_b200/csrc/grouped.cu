@@ -420,6 +420,16 @@ __device__ __forceinline__ void add_parts(const float* p, size_t stride, int par
   }
 }
 
+// silu(g) m.  With h = exp(-|g| / 2) it is g m / (1 + h^2) for g >= 0 and
+// g h m h / (1 + h^2) below: the divisor stays in [1, 2], and no factor leaves
+// the range of fp32 before the result does (exp(-g) overflows from g = -88.7
+// on, and a quick division by more than 2^126 gives zero).
+__device__ __forceinline__ float silu_times(float g, float m) {
+  const float h = expf(-0.5f * fabsf(g));
+  const float q = __fdividef(g < 0.0f ? g * h : g, fmaf(h, h, 1.0f)) * m;
+  return g < 0.0f ? q * h : q;
+}
+
 template <int kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     tiles_kernel(const __grid_constant__ Maps maps, const TileArgs a) {
@@ -697,7 +707,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; i++) {
             const float o = in[i][lane], g = up ? o : v[2 * i], m = up ? v[2 * i + 1] : o;
-            r[i] = __fdividef(g, 1.0f + __expf(-g)) * m;
+            r[i] = silu_times(g, m);
           }
           const int* q_of = s.y_row + (up ? kMaxCols / 2 : 0) + (j0 >> 1);
           const int cw = (t.c0 * 2 + rank) * kChan + (q4 & 1) * 32;
