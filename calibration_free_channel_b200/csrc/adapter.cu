@@ -152,7 +152,8 @@ __global__ void __launch_bounds__(512) z_kernel(AdapterArgs a, size_t z_rows) {
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kKWarps; w++) v += red[(w * kRowsZ + row) * kCols + j];
-      v *= scale;
+      const int p = q0 + row;  // (a row that is not the adapter's: zeros times its weights may be NaN)
+      v = p >= p0 && p < p1 ? v * scale : 0.0f;
       const uint16_t hi16 = f2bf16(v);
       const float left = v - bf16f(hi16);
       const size_t at = ((size_t)u * kRowsZ + row) * r + j;
