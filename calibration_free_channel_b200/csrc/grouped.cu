@@ -117,6 +117,9 @@ struct TileArgs {
   // adapters (G of them; the tiles run over all P rows)
   int r, has_w;
   const uint16_t* base;
+  const uint16_t* w;      // as Maps has them
+  const uint16_t* z;
+  const uint16_t* b;
   const float* scale;     // kLowRank
   size_t z_half;          // elements of one of z's halves
 };
@@ -308,6 +311,55 @@ __device__ __forceinline__ bool adapter_steps(const TileArgs& a, const Side& s, 
         if (!f(g, c, cols, kb, h, nh)) return false;
   }
   return true;
+}
+
+// Channel c of sorted position p from the definition, without the tensor cores
+// (and without base), for values that came out as NaN.  32 columns that several
+// adapters meet in get the products of each, for the positions that it does not
+// own with rows of zeros: nothing, unless its B_g is not finite there, and NaN
+// then.  And an infinity of B_g times the two terms of z may be infinities of
+// both signs; here the terms are added first.  Few values ever need it, and it
+// is slow: 64 values of K at a time, each lane on rows of its own (one such
+// adapter of 32, 64 tokens, 2048 x 2048: 2 ms a call instead of 25 us).
+__device__ __forceinline__ float own_sum(const TileArgs& a, const Side& s, int p, int c) {
+  int g = 0, hi = a.G;  // the first adapter that ends behind p
+  while (g < hi) {
+    const int m = (g + hi) >> 1;
+    if (s.first[m] + s.rows[m] > p)
+      hi = m;
+    else
+      g = m + 1;
+  }
+  auto add8 = [](uint4 x, uint4 rest, uint4 w, float& sum) {
+    const uint32_t xv[4] = {x.x, x.y, x.z, x.w}, rv[4] = {rest.x, rest.y, rest.z, rest.w}, wv[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      sum = fmaf(bf16lo(xv[i]) + bf16lo(rv[i]), bf16lo(wv[i]), sum);
+      sum = fmaf(bf16hi(xv[i]) + bf16hi(rv[i]), bf16hi(wv[i]), sum);
+    }
+  };
+  float sum = 0.0f;
+  if (g < a.G && s.first[g] <= p) {
+    pdl_wait();  // z
+    const uint16_t* z = a.z + (size_t)(s.before[g] + p - (s.first[g] & ~31)) * a.r;
+    const uint16_t* b = a.b + ((size_t)g * a.N + c) * a.r;
+    for (int j = 0; j < a.r; j += 8) {
+      add8(__ldcg(reinterpret_cast<const uint4*>(z + j)), __ldcg(reinterpret_cast<const uint4*>(z + a.z_half + j)),
+           __ldcg(reinterpret_cast<const uint4*>(b + j)), sum);
+    }
+  }
+  if (a.has_w) {
+    const int t = __ldcg(a.x_rows + p);
+    if (t < 0 || t >= a.n_x) return sum;  // recorded where its row was fetched
+    const uint16_t *x = a.x + (size_t)t * a.ldx, *w = a.w + (size_t)c * a.K;
+    for (int k0 = 0; k0 < a.K && sum == sum; k0 += 64)
+#pragma unroll
+      for (int k = k0; k < k0 + 64; k += 8)
+        if (k < a.K)
+          add8(__ldcg(reinterpret_cast<const uint4*>(x + k)), make_uint4(0u, 0u, 0u, 0u),
+               __ldcg(reinterpret_cast<const uint4*>(w + k)), sum);
+  }
+  return sum;
 }
 
 // The rows of x at sorted positions, gathered: thread i of 128 copies the
@@ -694,6 +746,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         } else {
           load_columns(j0, v);
         }
+        if (kMode == kAdapter) {
+          float some[4] = {};  // NaN if a value is (or if infinities meet)
+#pragma unroll
+          for (int j = 0; j < 32; j++) some[j & 3] += v[j];
+          const float sum = (some[0] + some[1]) + (some[2] + some[3]);
+          if (__any_sync(0xffffffffu, sum != sum)) {
+            const int c = (t.c0 * 2 + rank) * kChan + q4 * 32 + lane;
+#pragma unroll 1
+            for (int i = 0; i < 32 && j0 + i < t.n; i++) {
+              float old = 0.0f;
+#pragma unroll
+              for (int j = 0; j < 32; j++) old = j == i ? v[j] : old;
+              if (c < a.N && old != old) {
+                const float now = own_sum(a, s, t.p0 + j0 + i, c);
+#pragma unroll
+                for (int j = 0; j < 32; j++) v[j] = j == i ? now : v[j];
+              }
+              __syncwarp();
+            }
+          }
+        }
         if (kMode == kSwiglu) {
           // the gate side finishes the even columns, the up side the odd ones
           const bool up = q4 >= 2;
@@ -984,6 +1057,10 @@ cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s) {
   t.count = static_cast<uint32_t*>(a.split);
   t.part = reinterpret_cast<float*>(static_cast<char*>(a.split) + align256(sizeof(uint32_t) * 2 * kMaxPairs));
   t.r = a.r;
+  t.w = a.w;
+  t.z = a.z;
+  t.b = a.b;
+  t.z_half = zr * a.r;
   t.has_w = a.w != nullptr;
   t.base = a.base;
   t.cols = choose_cols(a.T, 1, a.N, 2 * kLanes);

@@ -389,6 +389,9 @@ moe_status moe_reader_grouped_product(int n_groups, int n_rows, int n_x, int n_y
  * [T, N] bf16 or NULL, may be y itself; a [n_adapters, r, K], b [n_adapters,
  * N, r] bf16; scale [n_adapters] fp32 or NULL (1); y [T, N] bf16.
  * r in {8, 16, ..., 128}: an adapter of lower rank is padded with zeros.
+ * What an adapter's weights and scale hold reaches its own tokens only, NaN
+ * and infinities included (values beside such an adapter's tokens are then
+ * summed in another order than without it).
  * The low-rank product x A^T keeps 16 significant bits (two bf16 terms). */
 size_t moe_reader_adapter_workspace_bytes(int T, int n_adapters, int K, int N, int r);
 moe_status moe_reader_adapter_product(int T, int n_adapters, int N, int K, int r, const uint16_t* x,

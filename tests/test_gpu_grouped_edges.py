@@ -68,3 +68,101 @@ def test_adapters_down_side_nonfinite_stays_apart(T, A, bad):
     mine = ids == 1
     assert torch.equal(z[~mine], y[~mine])
     assert not bool(torch.isfinite(z[mine]).any()) or bad != "a nan"
+
+
+def adapter_ref(t, ids, N):
+    """The definition in 64 bits and what fp32 sums and two bf16 terms of z may differ by."""
+    x = t["x"].double()
+    K, r = t["a"].shape[2], t["a"].shape[1]
+    ref = torch.zeros((x.shape[0], N), dtype=torch.float64, device="cuda")
+    err = torch.zeros_like(ref)
+    if t["base"] is not None:
+        ref += t["base"].double()
+        err += 2.0 ** -24 * t["base"].double().abs()
+    if t["w"] is not None:
+        ref += x @ t["w"].double().T
+        err += sum_err(K) * (x.abs() @ t["w"].double().abs().T)
+    for g in range(t["a"].shape[0]):
+        q = (ids == g).nonzero().flatten()
+        if q.numel() == 0:
+            continue
+        s = 1.0 if t["scale"] is None else float(t["scale"][g])
+        z, b = s * (x[q] @ t["a"][g].double().T), t["b"][g].double()
+        ez = abs(s) * sum_err(K) * (x[q].abs() @ t["a"][g].double().abs().T) + (2.0 ** -16 + 2.0 ** -22) * z.abs()
+        ref[q] += z @ b.T
+        err[q] += ez @ b.abs().T + sum_err(2 * r + 8) * (z.abs() @ b.abs().T)
+    # the terms meet in one fp32 accumulator: a few roundings of the running value
+    return ref, HALF * ref.abs() + SLACK * (err + 2.0 ** -20 * ref.abs()) + 1e-30
+
+
+@pytest.mark.parametrize("T,A", [(2, 2), (3, 2), (64, 32), (90, 5), (700, 40), (2100, 5), (2300, 60)])
+@pytest.mark.parametrize("use_w,use_base,inplace", [(True, False, False), (False, True, True), (True, True, False)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_adapters_up_side_nonfinite_stays_apart(T, A, use_w, use_base, inplace, bad):
+    """Weights of B that are not finite reach the adapter's own tokens only, in the channels that have them."""
+    K, N, r = 264, 520, 24
+    y, ids, t = adapter_call(T, A, K, N, r, use_w=use_w, use_base=use_base)
+    b = t["b"].clone()
+    b[1, 0, 3] = b[1, 77, 0] = b[1, 78, 23] = b[1, 519, 8] = bad
+    b[1, 256:300] = -bad
+    z, _, _ = adapter_call(T, A, K, N, r, use_w=use_w, use_base=use_base, inplace=inplace, b=b)
+    mine = ids == 1
+    spoilt = ~torch.isfinite(b[1].float()).all(1)
+    close(z[~mine], *(v[~mine] for v in adapter_ref(t, ids, N)))
+    assert torch.equal(z[:, ~spoilt], y[:, ~spoilt])
+    assert not bool(torch.isfinite(z[mine][:, spoilt]).any())
+    # and the same bits again
+    again, _, _ = adapter_call(T, A, K, N, r, use_w=use_w, use_base=use_base, inplace=inplace, b=b)
+    assert torch.equal(z.view(torch.int16), again.view(torch.int16))
+
+
+def test_adapters_of_one_batch_all_but_one_nonfinite():
+    """Every block of 32 positions is met by adapters that are not finite in any weight, and a token by NaN of its own."""
+    T, A, K, N, r = 400, 7, 136, 264, 16
+    y, ids, t = adapter_call(T, A, K, N, r)
+    b, x = t["b"].clone(), t["x"].clone()
+    b[[0, 1, 3, 4, 5, 6]] = float("nan")
+    free = (ids == 2) | (ids == -1)
+    own = int(free.nonzero()[0])
+    x[own, 130] = float("nan")
+    z, _, _ = adapter_call(T, A, K, N, r, b=b, x=x)
+    free[own] = False
+    close(z[free], *(v[free] for v in adapter_ref(t, ids, N)))
+    assert not bool(torch.isfinite(z[~free]).any())
+
+
+@pytest.mark.parametrize("T,use_w", [(3, True), (64, True), (64, False)])
+def test_adapters_nonfinite_where_sums_are_split(T, use_w):
+    # few tiles over a long K: the parts of a sum, and of the adapters, meet
+    A, K, N, r = 3, 2048, 512, 72
+    y, ids, t = adapter_call(T, A, K, N, r, use_w=use_w, seed=7)
+    b = t["b"].clone()
+    b[1] = float("inf")
+    z, _, _ = adapter_call(T, A, K, N, r, use_w=use_w, seed=7, b=b)
+    mine = ids == 1
+    close(z[~mine], *(v[~mine] for v in adapter_ref(t, ids, N)))
+    assert not bool(torch.isfinite(z[mine]).any())
+
+
+def test_adapters_infinite_results_stay():
+    """Infinities that the definition has: a token's, a projection's, and both meeting."""
+    T, A, K, N, r = 50, 3, 64, 64, 8
+    y, ids, t = adapter_call(T, A, K, N, r)
+    w, b = t["w"].clone(), t["b"].clone()
+    w[5] = 0
+    w[5, 3] = float("inf")
+    b[0, 5] = 0
+    b[0, 5, 2] = float("inf")
+    b[1] = float("nan")
+    z, _, _ = adapter_call(T, A, K, N, r, b=b, w=w)
+    x, a, s = t["x"].double(), t["a"].double(), t["scale"]
+    for q in range(T):
+        g = int(ids[q])
+        if g == 1:
+            assert torch.isnan(z[q]).all()
+            continue
+        want = x[q, 3] * float("inf")
+        if g == 0:
+            want = want + (float(s[0]) * (a[0, 2] @ x[q])) * float("inf")
+        got = z[q, 5].double()
+        assert bool(torch.isnan(got)) if bool(torch.isnan(want)) else bool(got == want), (q, g, got, want)
