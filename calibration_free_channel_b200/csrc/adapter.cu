@@ -154,11 +154,11 @@ __global__ void __launch_bounds__(512) z_kernel(AdapterArgs a, size_t z_rows) {
       for (int w = 0; w < kKWarps; w++) v += red[(w * kRowsZ + row) * kCols + j];
       const int p = q0 + row;  // (a row that is not the adapter's: zeros times its weights may be NaN)
       v = p >= p0 && p < p1 ? v * scale : 0.0f;
-      const uint16_t hi16 = f2bf16(v);
-      const float left = v - bf16f(hi16);
       const size_t at = ((size_t)u * kRowsZ + row) * r + j;
-      a.z[at] = hi16;
-      a.z[z_rows * r + at] = isfinite(v) ? f2bf16(left) : (uint16_t)0;  // an infinity leaves no rest
+      uint32_t top, rest;
+      bf16_terms(v, 0.0f, top, rest);
+      a.z[at] = (uint16_t)top;
+      a.z[z_rows * r + at] = (uint16_t)rest;
     }
     __syncthreads();
   }

@@ -41,6 +41,18 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
+// Two fp32 as two bf16 terms each: the rounded value, and what that leaves,
+// rounded.  A finite value stays finite (the last half step below 2^128 would
+// round to infinity); an infinity or NaN leaves nothing.
+__device__ __forceinline__ float bf16_finite(float v) {
+  const float most = __uint_as_float(0x7f7f0000u);
+  return isfinite(v) ? fminf(fmaxf(v, -most), most) : v;
+}
+__device__ __forceinline__ void bf16_terms(float lo, float hi, uint32_t& top, uint32_t& rest) {
+  top = bf16x2(bf16_finite(lo), bf16_finite(hi));
+  rest = bf16x2(isfinite(lo) ? lo - bf16lo(top) : 0.0f, isfinite(hi) ? hi - bf16hi(top) : 0.0f);
+}
+
 // ------------------------------------------------------------ exp / SiLU
 // exp_r: Cody & Waite reduction t = n ln2 + r (ln 2 split into a
 // 16-significant-bit head and an fp32 tail), degree-7 Taylor polynomial of

@@ -709,7 +709,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           float rest[32];
           tmem_ld32(acc + ((t.n + 31) & ~31) + j0, rest);
 #pragma unroll
-          for (int j = 0; j < 32; j++) v[j] += rest[j];
+          for (int j = 0; j < 32; j++)  // (an infinite weight: the first term has its sign, the second may have the other)
+            v[j] = isfinite(v[j]) ? v[j] + rest[j] : v[j];
         }
       };
       bool finish = true;
@@ -798,14 +799,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               const float o = __shfl_xor_sync(0xffffffffu, odd ? r[i] : r[i + 1], 1);
-              const uint32_t p2 = odd ? bf16x2(o, r[i + 1]) : bf16x2(r[i], o);
+              const float lo = odd ? o : r[i], hi = odd ? r[i + 1] : o;
               const int q = q_of[i + (odd ? 1 : 0)];
-              st32_if(y + (size_t)q * a.ldy + c, p2, q >= 0 && in_n);
-              if (a.y_rest) {  // (an infinity leaves no rest)
-                const float lo = odd ? o : r[i], hi = odd ? r[i + 1] : o;
-                const float rl = isfinite(lo) ? lo - bf16lo(p2) : 0.0f, rh = isfinite(hi) ? hi - bf16hi(p2) : 0.0f;
-                st32_if(a.y_rest + (size_t)q * a.ldy + c, bf16x2(rl, rh), q >= 0 && in_n);
+              uint32_t p2 = bf16x2(lo, hi);
+              if (a.y_rest) {
+                uint32_t rest;
+                bf16_terms(lo, hi, p2, rest);
+                st32_if(a.y_rest + (size_t)q * a.ldy + c, rest, q >= 0 && in_n);
               }
+              st32_if(y + (size_t)q * a.ldy + c, p2, q >= 0 && in_n);
             }
           }
         } else if (kMode == kPlain && a.y_fp32) {
@@ -830,11 +832,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             const bool own = q >= 0, some = q != -1;
             if (!own) q = -2 - q;
             const float lo = own ? (odd ? o : v[2 * i]) * scale : 0.0f, hi = own ? (odd ? v[2 * i + 1] : o) * scale : 0.0f;
-            const uint32_t top = bf16x2(lo, hi);
-            // (an infinity leaves no rest)
-            const float rl = isfinite(lo) ? lo - bf16lo(top) : 0.0f, rh = isfinite(hi) ? hi - bf16hi(top) : 0.0f;
+            uint32_t top, rest;
+            bf16_terms(lo, hi, top, rest);
             st32_if(z + (size_t)q * a.N, top, some && in_n);
-            st32_if(z + a.z_half + (size_t)q * a.N, bf16x2(rl, rh), some && in_n);
+            st32_if(z + a.z_half + (size_t)q * a.N, rest, some && in_n);
           }
         } else {
           // two channels to a word: the even lane of a pair takes the even column

@@ -166,3 +166,60 @@ def test_adapters_infinite_results_stay():
             want = want + (float(s[0]) * (a[0, 2] @ x[q])) * float("inf")
         got = z[q, 5].double()
         assert bool(torch.isnan(got)) if bool(torch.isnan(want)) else bool(got == want), (q, g, got, want)
+
+
+# ------------------------------------------------ values held in two bf16 terms
+# Between the largest bf16 and 2^128 a value rounds to infinity, but its two
+# terms hold it.
+@pytest.mark.parametrize("T", [5, 100, 2100])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_adapters_two_terms_below_overflow(T, sign):
+    K, N, r = 64, 64, 8
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device="cuda")
+    a = torch.zeros((1, r, K), dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1] = sign * 255 * 2.0 ** 57, sign * 1.5 * 2.0 ** 60
+    a[0, :, 0], a[0, :, 1] = 2.0 ** 63, 2.0 ** 59  # z = 0x1.ffp127 and half a step of 2^119 more
+    b = torch.zeros((1, N, r), dtype=torch.bfloat16, device="cuda")
+    b[0, :, 3] = 2.0 ** -100
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+    y, _, t = adapter_call(T, 1, K, N, r, use_w=False, use_base=False, ids=ids, x=x, a=a, b=b, scale=None)
+    close(y, *adapter_ref(t, ids, N))
+
+
+def one_expert(d=256, I=16, E=1):
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    return dict(w_router=z(E, d), router_bias=None, w_gate=z(E, I, d), w_up=z(E, I, d), w_down=z(E, I, d))
+
+
+@pytest.mark.parametrize("B", [1, 40, 64])
+def test_block_two_terms_below_overflow(B):
+    W = one_expert()
+    x = torch.zeros((B, 256), dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1], x[:, 2] = 1.96875 * 2.0 ** 63, 2.0 ** 64, 1.875 * 2.0 ** 57
+    W["w_gate"][0, 3, 0] = W["w_up"][0, 3, 1] = W["w_up"][0, 3, 2] = 1.0  # silu(g) u = 1.9976 2^127
+    W["w_down"][0, 3] = 2.0 ** -110
+    L = M.Layer(W, top_e=1)
+    y = L.forward_grouped(x)
+    L.check()
+    a = 1.96875 * 2.0 ** 63 * (2.0 ** 64 + 1.875 * 2.0 ** 57)
+    ref = torch.full((B, 256), a * 2.0 ** -110, dtype=torch.float64, device="cuda")
+    close(y, ref, (HALF + 2.0 ** -15) * ref)
+
+
+@pytest.mark.parametrize("B", [3, 60, 200])
+def test_block_infinite_down_weights_keep_their_sign(B):
+    # two terms (few tokens an expert) or one: a x inf is an infinity of a's sign
+    E, I, d = 2, 16, 256
+    W = dict(one_expert(E=E), w_gate=dev(E, I, d, seed=3), w_up=dev(E, I, d, seed=4), w_down=dev(E, I, d, seed=5))
+    W["w_down"][:, 7, 9] = float("inf")
+    W["w_down"][:, 2, 11] = -float("inf")
+    x = dev(B, d, seed=6, scale=0.1)
+    L = M.Layer(W, top_e=1)
+    y = L.forward_grouped(x).double()
+    L.check()
+    # zero router rows: expert 0 for every token
+    g, u = x.double() @ W["w_gate"][0].double().T, x.double() @ W["w_up"][0].double().T
+    s = torch.sign(g) * torch.sign(u)
+    inf = torch.full((B,), float("inf"), dtype=torch.float64, device="cuda")
+    assert torch.equal(y[:, 9], s[:, 7] * inf) and torch.equal(y[:, 11], -s[:, 2] * inf)
+    assert torch.isfinite(y[:, 12:]).all()
