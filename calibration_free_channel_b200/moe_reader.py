@@ -121,21 +121,50 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_cuda_set_up = False
+
+
+def _device():
+    """The current device's index, None before torch has set CUDA up."""
+    global _cuda_set_up
+    if not _cuda_set_up:
+        if not torch.cuda.is_initialized():
+            return None
+        _cuda_set_up = True
+    return torch._C._cuda_getDevice()
+
+
+# what the grouped entry points' arrays may hold (bf16 also as bit patterns)
+_BF16 = frozenset((torch.bfloat16, torch.uint16, torch.int16))
+_I32 = frozenset((torch.int32, torch.uint32))
+_F32 = frozenset((torch.float32,))
+
+
 def _ptrs(*args):
-    """Pointers of the grouped entry points' arrays: tensors have to be
-    contiguous and on the current device (a strided, host or other device's
-    tensor would have the kernels read memory that is not its values)."""
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
+    """Pointers of the grouped entry points' arrays, each given as (tensor or
+    address, its types, the elements it must have) or, for a workspace, as
+    (tensor or address, None, bytes).  Tensors have to be contiguous, on the
+    current device, of such a type and large enough: the kernels would read or
+    write memory that is not their values otherwise."""
+    dev = _device()
     out = []
-    for t in args:
+    for t, types, n in args:
         if t is None or type(t) is int:
             out.append(t)
-        elif t.get_device() == dev and t.is_contiguous():
+        elif (t.get_device() == dev and t.is_contiguous() and
+              (t.nbytes >= n if types is None else t.dtype in types and t.numel() >= n)):
             out.append(t.data_ptr())
         elif t.get_device() != dev:
             raise MoeError(MOE_EINVAL, f"a tensor is on {t.device}, not on the current CUDA device")
-        else:
+        elif not t.is_contiguous():
             raise MoeError(MOE_EINVAL, f"a tensor of shape {tuple(t.shape)} is not contiguous")
+        elif types is None:
+            raise MoeError(MOE_EINVAL, f"a workspace has {t.nbytes} bytes, less than the {n} it is said to have")
+        elif t.dtype not in types:
+            raise MoeError(MOE_EINVAL, f"a tensor of shape {tuple(t.shape)} is {t.dtype}: use " +
+                           " or ".join(sorted(str(d) for d in types)))
+        else:
+            raise MoeError(MOE_EINVAL, f"a tensor of shape {tuple(t.shape)} has {t.numel()} elements of {n}")
     return out
 
 
@@ -143,7 +172,8 @@ def _stream(stream):
     if stream is None:
         # the current stream's handle without building a Stream object (which costs more than a launch);
         # before torch has set CUDA up, that is the default stream
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if torch.cuda.is_initialized() else None
+        dev = _device()
+        return torch._C._cuda_getCurrentRawStream(dev) if dev is not None else None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -216,7 +246,8 @@ def moe_reader_group_workspace_bytes(n, n_groups) -> int:
 
 
 def moe_reader_group_rows(n, n_groups, ids, offsets, rows, workspace, ws_bytes, stream=None):
-    _check(lib().moe_reader_group_rows(n, n_groups, *_ptrs(ids, offsets, rows, workspace), ws_bytes, _stream(stream)))
+    p = _ptrs((ids, _I32, n), (offsets, _I32, n_groups + 1), (rows, _I32, n), (workspace, None, ws_bytes))
+    _check(lib().moe_reader_group_rows(n, n_groups, *p, ws_bytes, _stream(stream)))
 
 
 def moe_reader_grouped_workspace_bytes(n_groups, n_rows) -> int:
@@ -225,14 +256,18 @@ def moe_reader_grouped_workspace_bytes(n_groups, n_rows) -> int:
 
 def moe_reader_grouped_swiglu(n_groups, n_rows, n_x, I, d, x, x_rows, x_div, offsets, w_gate, w_up, a, workspace,
                               ws_bytes, stream=None):
-    x, x_rows, *rest = _ptrs(x, x_rows, offsets, w_gate, w_up, a, workspace)
+    x, x_rows, *rest = _ptrs((x, _BF16, n_x * d), (x_rows, _I32, n_rows), (offsets, _I32, n_groups + 1),
+                             (w_gate, _BF16, n_groups * I * d), (w_up, _BF16, n_groups * I * d),
+                             (a, _BF16, n_rows * I), (workspace, None, ws_bytes))
     _check(lib().moe_reader_grouped_swiglu(n_groups, n_rows, n_x, I, d, x, x_rows, x_div, *rest, ws_bytes,
                                            _stream(stream)))
 
 
 def moe_reader_grouped_product(n_groups, n_rows, n_x, n_y, N, K, w_layout, x, x_rows, x_div, offsets, w, y, y_rows,
                                workspace, ws_bytes, stream=None):
-    x, x_rows, *rest = _ptrs(x, x_rows, offsets, w, y, y_rows, workspace)
+    x, x_rows, *rest = _ptrs((x, _BF16, n_x * K), (x_rows, _I32, n_rows), (offsets, _I32, n_groups + 1),
+                             (w, _BF16, n_groups * N * K), (y, _BF16, n_y * N), (y_rows, _I32, n_rows),
+                             (workspace, None, ws_bytes))
     _check(lib().moe_reader_grouped_product(n_groups, n_rows, n_x, n_y, N, K, w_layout, x, x_rows, x_div, *rest,
                                             ws_bytes, _stream(stream)))
 
@@ -243,9 +278,10 @@ def moe_reader_adapter_workspace_bytes(T, n_adapters, K, N, r) -> int:
 
 def moe_reader_adapter_product(T, n_adapters, N, K, r, x, w, base, offsets, rows, a, b, scale, y, workspace, ws_bytes,
                                stream=None):
-    _check(lib().moe_reader_adapter_product(T, n_adapters, N, K, r,
-                                            *_ptrs(x, w, base, offsets, rows, a, b, scale, y, workspace), ws_bytes,
-                                            _stream(stream)))
+    p = _ptrs((x, _BF16, T * K), (w, _BF16, N * K), (base, _BF16, T * N), (offsets, _I32, n_adapters + 1),
+              (rows, _I32, T), (a, _BF16, n_adapters * r * K), (b, _BF16, n_adapters * N * r),
+              (scale, _F32, n_adapters), (y, _BF16, T * N), (workspace, None, ws_bytes))
+    _check(lib().moe_reader_adapter_product(T, n_adapters, N, K, r, *p, ws_bytes, _stream(stream)))
 
 
 def moe_reader_block_workspace_bytes(B, E, top_e, I, d) -> int:
@@ -253,8 +289,10 @@ def moe_reader_block_workspace_bytes(B, E, top_e, I, d) -> int:
 
 
 def moe_reader_forward_grouped(layer: MoeReaderLayer, B, x, residual, y, ids, workspace, ws_bytes, stream=None):
-    _check(lib().moe_reader_forward_grouped(C.byref(layer), B, *_ptrs(x, residual, y, ids, workspace), ws_bytes,
-                                            _stream(stream)))
+    n = B * layer.d
+    p = _ptrs((x, _BF16, n), (residual, _BF16, n), (y, _BF16, n), (ids, _I32, B * layer.top_e),
+              (workspace, None, ws_bytes))
+    _check(lib().moe_reader_forward_grouped(C.byref(layer), B, *p, ws_bytes, _stream(stream)))
 
 
 def moe_reader_rmsnorm(B, d, eps, x, h, stream=None):
@@ -456,9 +494,16 @@ class Layer:
         return y
 
     def forward_grouped(self, x, residual=None, ids=None, stream=None, out=None):
-        """The all-channel block over any number of tokens (prompts): ids, if
-        given, receives the chosen experts ([B, top_e] int32)."""
+        """The all-channel block over any number of tokens (prompts): x,
+        residual and out [B, d] bf16; ids, if given, receives the chosen
+        experts ([B, top_e] int32)."""
         B = x.shape[0]
+        for name, t, shape in (("x", x, (B, self.d)), ("residual", residual, (B, self.d)), ("out", out, (B, self.d)),
+                               ("ids", ids, (B, self.top_e))):
+            if t is not None and tuple(t.shape) != shape:
+                raise MoeError(MOE_EINVAL, f"{name} has shape {tuple(t.shape)}, not {shape}")
+        if x.device != self.w["w_gate"].device:
+            raise MoeError(MOE_EINVAL, f"x is on {x.device}, the layer on {self.w['w_gate'].device}")
         nb = moe_reader_block_workspace_bytes(B, self.E, self.top_e, self.I, self.d)
         if self._wsg is None or self._wsg.numel() < nb:
             self._wsg = torch.zeros(max(nb, 16), dtype=torch.uint8, device=x.device)

@@ -223,3 +223,30 @@ def test_block_infinite_down_weights_keep_their_sign(B):
     inf = torch.full((B,), float("inf"), dtype=torch.float64, device="cuda")
     assert torch.equal(y[:, 9], s[:, 7] * inf) and torch.equal(y[:, 11], -s[:, 2] * inf)
     assert torch.isfinite(y[:, 12:]).all()
+
+
+# ---------------------------------------------------------- calls and shapes
+def test_block_refuses_other_shapes_and_types():
+    L = M.Layer(one_expert(E=3), top_e=2)
+    x = dev(40, 256, seed=1)
+    ids = torch.zeros((40, 2), dtype=torch.int32, device="cuda")
+    y = L.forward_grouped(x, x, ids)
+    wrong = [dict(x=x[:, :128].contiguous()), dict(x=x.view(80, 128)), dict(x=x.view(1, 40, 256)), dict(x=x.float()),
+             dict(x=x.half()), dict(x=x.t()), dict(residual=x[:39]), dict(residual=x.float()), dict(out=y[:39]),
+             dict(out=torch.empty(40, 256, device="cuda")), dict(ids=ids.long()), dict(ids=ids[:39]),
+             dict(ids=ids[:, :1].contiguous()), dict(x=x.cpu())]
+    for kw in wrong:
+        with pytest.raises(M.MoeError, match="MOE_EINVAL"):
+            L.forward_grouped(**dict(dict(x=x), **kw))
+    L.check()
+    assert torch.equal(y, L.forward_grouped(x.view(torch.int16), x.view(torch.int16)).view(torch.bfloat16))
+
+
+def test_plan_refuses_64_bit_ids():
+    ids = torch.randint(0, 8, (64,), device="cuda")
+    off, rows = torch.zeros(9, dtype=torch.int32, device="cuda"), torch.zeros(64, dtype=torch.int32, device="cuda")
+    ws = ws_for(M.moe_reader_group_workspace_bytes(64, 8))
+    with pytest.raises(M.MoeError, match="MOE_EINVAL.*int64"):
+        M.moe_reader_group_rows(64, 8, ids, off, rows, ws, ws.numel())
+    M.moe_reader_group_rows(64, 8, ids.int(), off, rows, ws, ws.numel())
+    assert torch.equal(rows.long(), torch.sort(ids, stable=True).indices)

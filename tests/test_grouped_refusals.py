@@ -115,3 +115,70 @@ def test_workspace_queries(lib):
     assert M.moe_reader_grouped_workspace_bytes(1025, 1) == 0
     assert M.moe_reader_adapter_workspace_bytes(1, 1, 2048, 2048, 136) == 0
     assert M.moe_reader_block_workspace_bytes(40000, 128, 8, 768, 2048) == 0
+
+
+# ------------------------------------------------- what the binding refuses
+class Fake:
+    """What the binding asks of a tensor, on the device it takes for the current one before CUDA is set up."""
+
+    def __init__(self, n, dtype, contiguous=True):
+        self.shape, self.dtype, self.contiguous = (n,), dtype, contiguous
+        self.nbytes = n * dtype.itemsize
+
+    def get_device(self):
+        return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def numel(self):
+        return self.shape[0]
+
+    def data_ptr(self):
+        raise AssertionError("a refused tensor's address was taken")
+
+
+BF, I32, F32, I64 = torch.bfloat16, torch.int32, torch.float32, torch.int64
+WRONG = {"type": "use torch", "elements": "elements of", "contiguous": "not contiguous"}
+
+
+def _wrong(how, n, dtype):
+    if how == "type":
+        return Fake(n, {BF: torch.float16, I32: I64, F32: torch.float64}[dtype])
+    return Fake(n - 1, dtype) if how == "elements" else Fake(n, dtype, contiguous=False)
+
+
+BINDING = {
+    "moe_reader_group_rows": (dict(n=64, n_groups=8, ids=F, offsets=F, rows=F, workspace=F, ws_bytes=BIG),
+                              dict(ids=(64, I32), offsets=(9, I32), rows=(64, I32))),
+    "moe_reader_grouped_swiglu": (dict(n_groups=8, n_rows=64, n_x=32, I=128, d=256, x=F, x_rows=F, x_div=2, offsets=F,
+                                       w_gate=F, w_up=F, a=F, workspace=F, ws_bytes=BIG),
+                                  dict(x=(32 * 256, BF), x_rows=(64, I32), offsets=(9, I32), w_gate=(8 * 128 * 256, BF),
+                                       w_up=(8 * 128 * 256, BF), a=(64 * 128, BF))),
+    "moe_reader_grouped_product": (dict(n_groups=8, n_rows=64, n_x=32, n_y=70, N=128, K=256, w_layout=0, x=F, x_rows=F,
+                                        x_div=2, offsets=F, w=F, y=F, y_rows=F, workspace=F, ws_bytes=BIG),
+                                   dict(x=(32 * 256, BF), x_rows=(64, I32), offsets=(9, I32), w=(8 * 128 * 256, BF),
+                                        y=(70 * 128, BF), y_rows=(64, I32))),
+    "moe_reader_adapter_product": (dict(T=64, n_adapters=8, N=128, K=256, r=16, x=F, w=F, base=F, offsets=F, rows=F,
+                                        a=F, b=F, scale=F, y=F, workspace=F, ws_bytes=BIG),
+                                   dict(x=(64 * 256, BF), w=(128 * 256, BF), base=(64 * 128, BF), offsets=(9, I32),
+                                        rows=(64, I32), a=(8 * 16 * 256, BF), b=(8 * 128 * 16, BF), scale=(8, F32),
+                                        y=(64 * 128, BF))),
+    "moe_reader_forward_grouped": (dict(layer=_layer(), B=300, x=F, residual=F, y=F, ids=F, workspace=F, ws_bytes=BIG),
+                                   dict(x=(300 * 256, BF), residual=(300 * 256, BF), y=(300 * 256, BF),
+                                        ids=(600, I32))),
+}
+
+
+@pytest.mark.parametrize("how", list(WRONG))
+@pytest.mark.parametrize("name,arg", [(f, a) for f in BINDING for a in BINDING[f][1]])
+def test_the_binding_refuses_what_is_not_the_array(name, arg, how):
+    args, arrays = BINDING[name]
+    with pytest.raises(M.MoeError, match="MOE_EINVAL.*" + WRONG[how]):
+        getattr(M, name)(**dict(args, **{arg: _wrong(how, *arrays[arg])}))
+
+
+@pytest.mark.parametrize("name", list(BINDING))
+def test_the_binding_refuses_a_workspace_that_is_smaller_than_said(name):
+    with pytest.raises(M.MoeError, match="MOE_EINVAL.*workspace"):
+        getattr(M, name)(**dict(BINDING[name][0], workspace=Fake(1 << 20, torch.uint8), ws_bytes=(1 << 20) + 1))
