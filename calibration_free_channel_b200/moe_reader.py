@@ -6,6 +6,7 @@ built, importing the functions raises; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -343,8 +344,9 @@ class Layer:
         self.alpha_up = torch.empty_like(self.alpha_gate)
         self.u_sigma = None
         self.v = None
-        self._ws = None
+        self._ws = None        # workspaces of the reader and of forward_grouped (see _scratch)
         self._wsg = None
+        self._captured = []
         self.path = 0          # which reader runs a sparse step (see struct)
         self.sketch_format = 0  # 0: 2-bit codes, 1: base 3 (build_sketch(packing=...))
         # [E] int32 weight slot of each expert (held experts only, compacted), or None
@@ -435,13 +437,76 @@ class Layer:
         S.expert_slot = slot.to(dev)
         S.E_held = int(own.numel())
         S._ws = S._wsg = None
+        S._captured = []
         return S
 
-    def workspace(self, B: int):
-        nb = moe_reader_workspace_bytes(B, self.E, self.top_e, self.I, self.d, 1, 1, self.r)
-        if self._ws is None or self._ws.numel() < nb:
-            self._ws = torch.zeros(nb, dtype=torch.uint8, device=self.w["w_gate"].device)
-        return self._ws
+    def _scratch(self, pool: str, nb: int, handle):
+        """The layer's workspace of at least nb bytes for calls on the stream
+        `handle`, which has to be the current one: it is allocated, zeroed and,
+        once a longer call replaces it, freed in that stream's order.  Calls on
+        two streams never share one.
+
+        A captured call gets one that eager calls no longer use and that lives
+        as long as the layer: of an earlier capture, or an eager one of before
+        the capture; without any, memory of the graph that each replay zeroes."""
+        held = getattr(self, pool)
+        if held is None:
+            held = {}
+            setattr(self, pool, held)
+        if torch.cuda.is_current_stream_capturing():
+            for p, zeroed, ws in self._captured:
+                if p == pool and zeroed and ws.numel() >= nb:
+                    return ws
+            for h, ws in held.items():
+                if ws.numel() >= nb:
+                    del held[h]
+                    self._captured.append((pool, True, ws))
+                    return ws
+            ws = torch.zeros(nb, dtype=torch.uint8, device=self.w["w_gate"].device)
+            self._captured.append((pool, False, ws))
+            return ws
+        ws = held.get(handle)
+        if ws is None or ws.numel() < nb:
+            new = torch.zeros(nb, dtype=torch.uint8, device=self.w["w_gate"].device)
+            if ws is not None:
+                new[:4].copy_(ws[:4])  # the error word
+            held[handle] = ws = new
+        return ws
+
+    @contextlib.contextmanager
+    def _elsewhere(self, side, tensors):
+        """Makes `side` the current stream, so that what a call allocates is in
+        that stream's order; the caching allocator then learns of its use of
+        tensors from elsewhere, and of the caller's use of what it returns."""
+        back = torch.cuda.current_stream(side.device)
+        made = []
+        with torch.cuda.stream(side):
+            yield made
+        for t in tensors:
+            if t is not None:
+                t.record_stream(side)
+        for t in made:
+            t.record_stream(back)
+
+    def _on(self, stream, *tensors):
+        """(handle, context) of a call on `stream` (None: the current one) that
+        uses `tensors`; the context takes the list of tensors it returns."""
+        handle = _stream(stream) or 0
+        if stream is None or handle == _stream(None):
+            return handle, contextlib.nullcontext([])
+        if not isinstance(stream, torch.cuda.Stream):
+            dev = self.w["w_gate"].device
+            stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+        return handle, self._elsewhere(stream, tensors)
+
+    def _reader_bytes(self, B):
+        return moe_reader_workspace_bytes(B, self.E, self.top_e, self.I, self.d, 1, 1, self.r)
+
+    def workspace(self, B: int, stream=None):
+        """The reader's workspace for steps of up to B tokens on `stream`."""
+        handle, on = self._on(stream)
+        with on:
+            return self._scratch("_ws", self._reader_bytes(B), handle)
 
     def _debug(self, B, k, c, dev):
         P = (B, self.top_e)
@@ -465,11 +530,14 @@ class Layer:
         """This rank's fp32 partial of the block ([B, d]) over the experts
         e % ep_size == ep_rank; sum it over the ranks, then ep_finish."""
         B = x.shape[0]
-        ws = self.workspace(B)
-        yp = out if out is not None else torch.empty((B, self.d), dtype=torch.float32, device=x.device)
-        dbg_t, dbg = self._debug(B, k, c, x.device) if debug else (None, None)
-        moe_reader_forward_ep(self.struct(r, recovery_input), B, k, c, x, ep_rank, ep_size, yp, dbg, ws, ws.numel(),
-                              stream)
+        handle, on = self._on(stream, x, out)
+        with on as made:
+            ws = self._scratch("_ws", self._reader_bytes(B), handle)
+            yp = out if out is not None else torch.empty((B, self.d), dtype=torch.float32, device=x.device)
+            dbg_t, dbg = self._debug(B, k, c, x.device) if debug else (None, None)
+            moe_reader_forward_ep(self.struct(r, recovery_input), B, k, c, x, ep_rank, ep_size, yp, dbg, ws,
+                                  ws.numel(), handle)
+            made += [yp, *(dbg_t or {}).values()]
         return (yp, dbg_t) if debug else yp
 
     def forward(self, x, k: int, c: int, residual=None, debug: bool = False, r: int | None = None, stream=None,
@@ -477,26 +545,33 @@ class Layer:
         """events: (ev_before, ev_after) torch.cuda.Event recorded around the
         expert kernels (timing only; not with debug)."""
         B = x.shape[0]
-        ws = self.workspace(B)
-        y = out if out is not None else torch.empty_like(x)
-        dbg_t, dbg = self._debug(B, k, c, x.device) if debug else (None, None)
-        if events is not None:
-            dbg = timing_debug(*events)
-        moe_reader_forward(self.struct(r, recovery_input, path), B, k, c, x, residual, y, dbg, ws, ws.numel(),
-                           stream)
+        handle, on = self._on(stream, x, residual, out)
+        with on as made:
+            ws = self._scratch("_ws", self._reader_bytes(B), handle)
+            y = out if out is not None else torch.empty_like(x)
+            dbg_t, dbg = self._debug(B, k, c, x.device) if debug else (None, None)
+            if events is not None:
+                dbg = timing_debug(*events)
+            moe_reader_forward(self.struct(r, recovery_input, path), B, k, c, x, residual, y, dbg, ws, ws.numel(),
+                               handle)
+            made += [y, *(dbg_t or {}).values()]
         return (y, dbg_t) if debug else y
 
     def forward_dense(self, x, residual=None, stream=None, out=None):
         B = x.shape[0]
-        ws = self.workspace(B)
-        y = out if out is not None else torch.empty_like(x)
-        moe_reader_forward_dense(self.struct(0), B, x, residual, y, ws, ws.numel(), stream)
+        handle, on = self._on(stream, x, residual, out)
+        with on as made:
+            ws = self._scratch("_ws", self._reader_bytes(B), handle)
+            y = out if out is not None else torch.empty_like(x)
+            moe_reader_forward_dense(self.struct(0), B, x, residual, y, ws, ws.numel(), handle)
+            made.append(y)
         return y
 
     def forward_grouped(self, x, residual=None, ids=None, stream=None, out=None):
         """The all-channel block over any number of tokens (prompts): x,
         residual and out [B, d] bf16; ids, if given, receives the chosen
-        experts ([B, top_e] int32)."""
+        experts ([B, top_e] int32). The layer
+        keeps a workspace for each stream it is called on."""
         B = x.shape[0]
         for name, t, shape in (("x", x, (B, self.d)), ("residual", residual, (B, self.d)), ("out", out, (B, self.d)),
                                ("ids", ids, (B, self.top_e))):
@@ -505,14 +580,25 @@ class Layer:
         if x.device != self.w["w_gate"].device:
             raise MoeError(MOE_EINVAL, f"x is on {x.device}, the layer on {self.w['w_gate'].device}")
         nb = moe_reader_block_workspace_bytes(B, self.E, self.top_e, self.I, self.d)
-        if self._wsg is None or self._wsg.numel() < nb:
-            self._wsg = torch.zeros(max(nb, 16), dtype=torch.uint8, device=x.device)
-        y = out if out is not None else torch.empty_like(x)
         with torch.cuda.device(x.device):
-            moe_reader_forward_grouped(self.struct(0), B, x, residual, y, ids, self._wsg, self._wsg.numel(), stream)
+            handle, on = self._on(stream, x, residual, out, ids)
+            with on as made:
+                ws = self._scratch("_wsg", max(nb, 16), handle)
+                y = out if out is not None else torch.empty_like(x)
+                moe_reader_forward_grouped(self.struct(0), B, x, residual, y, ids, ws, ws.nbytes, handle)
+                made.append(y)
         return y
 
     def check(self, stream=None):
-        for ws in (self._ws, self._wsg):
-            if ws is not None:
-                moe_reader_check_error(ws, stream)
+        """Raises what the layer's calls recorded on the device since the last
+        check; waits for `stream` and for the streams that they ran on."""
+        found = None
+        held = [(h, ws) for pool in (self._ws, self._wsg) for h, ws in (pool or {}).items()]
+        for h, ws in held + [(None, ws) for _, _, ws in self._captured]:
+            for s in (stream,) if h is None or h == _stream(stream) else (stream, h):
+                try:
+                    moe_reader_check_error(ws, s)
+                except MoeError as e:
+                    found = found or e
+        if found is not None:
+            raise found

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from calibration_free_channel_b200 import moe_reader as M
-from tests.test_gpu_grouped import HALF, SLACK, close, dev, plan_of, swiglu_ref, sum_err, ws_for
+from calibration_free_channel_b200 import synth
+from tests.test_gpu_grouped import HALF, SLACK, block_ref, close, dev, plan_of, swiglu_ref, sum_err, ws_for
 
 pytestmark = pytest.mark.gpu
 
@@ -250,3 +251,160 @@ def test_plan_refuses_64_bit_ids():
         M.moe_reader_group_rows(64, 8, ids, off, rows, ws, ws.numel())
     M.moe_reader_group_rows(64, 8, ids.int(), off, rows, ws, ws.numel())
     assert torch.equal(rows.long(), torch.sort(ids, stable=True).indices)
+
+
+# ------------------------------------------------- streams, growth, captures
+SHAPE = synth.BlockShape(16, 256, 1024, 4)
+
+
+def small_layer(seed=24):
+    return M.Layer(synth.layer_weights(SHAPE, seed=seed, device="cuda"), top_e=4)
+
+
+def tokens_of(*lengths):
+    return [synth.tokens(1024, n, seed=40 + i).cuda() for i, n in enumerate(lengths)]
+
+
+def leave_bytes(nb, *streams):
+    """Memory that the allocator hands out next on these streams (and the current one) is full of ones."""
+    for s in (torch.cuda.current_stream(), *streams):
+        with torch.cuda.stream(s):
+            junk = [torch.full((nb,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+            del junk
+    torch.cuda.synchronize()
+
+
+def keep_busy():
+    torch.cuda._sleep(20_000_000)  # about 10 ms on the current stream
+
+
+def test_block_on_a_side_stream_first_and_longer():
+    """Workspace and output are made in the order of the stream that the call runs on, whatever the current one does."""
+    xs = tokens_of(40, 33, 300, 900)
+    L = small_layer()
+    want = [L.forward_grouped(x) for x in xs]
+    L.check()
+    side = small_layer()
+    s = torch.cuda.Stream()
+    leave_bytes(M.moe_reader_block_workspace_bytes(900, SHAPE.E, 4, SHAPE.I, SHAPE.d), s)
+    for x, w in zip(xs, want):
+        torch.cuda.synchronize()
+        keep_busy()
+        y = side.forward_grouped(x, stream=s)
+        s.synchronize()
+        assert torch.equal(y, w)
+        y = side.forward_grouped(x, stream=s.cuda_stream)  # a raw handle
+        s.synchronize()
+        assert torch.equal(y, w)
+    side.check()
+
+
+def test_block_of_one_layer_on_two_streams():
+    xs = tokens_of(500, 37, 260)
+    L = small_layer()
+    want = [L.forward_grouped(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        outs = [L.forward_grouped(x, stream=s) for x, s in zip(xs, streams)]
+        torch.cuda.synchronize()
+        for y, w in zip(outs, want):
+            assert torch.equal(y, w)
+    L.check()
+
+
+def test_block_inputs_may_be_dropped_behind_a_side_stream_call():
+    x, = tokens_of(700)
+    L = small_layer()
+    want = L.forward_grouped(x)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        t = x.clone()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            keep_busy()
+        outs.append(L.forward_grouped(t, stream=s))
+        del t
+        torch.full((700, 1024), float("nan"), dtype=torch.bfloat16, device="cuda")  # where t was, if it may be
+    torch.cuda.synchronize()
+    for y in outs:
+        assert torch.equal(y, want)
+
+
+def test_captured_block_outlives_longer_prompts():
+    """A graph keeps its workspace: longer calls, other calls at the same time and freed memory leave it alone."""
+    x, longer = tokens_of(120, 1500)
+    L = small_layer()
+    want, want2 = L.forward_grouped(x), None
+    y = torch.empty_like(x)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        L.forward_grouped(x, out=y)
+    want2 = L.forward_grouped(longer)
+    torch.cuda.synchronize()
+    leave_bytes(M.moe_reader_block_workspace_bytes(120, SHAPE.E, 4, SHAPE.I, SHAPE.d))
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        y.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            g.replay()
+        z = L.forward_grouped(x)  # beside the replay
+        z2 = L.forward_grouped(longer)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(z, want) and torch.equal(z2, want2)
+    L.check()
+
+
+def test_captured_block_without_a_call_before():
+    x, = tokens_of(50)
+    L = small_layer()
+    leave_bytes(M.moe_reader_block_workspace_bytes(50, SHAPE.E, 4, SHAPE.I, SHAPE.d))
+    ys = [torch.empty_like(x) for _ in range(3)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    with torch.cuda.graph(graphs[0]):
+        L.forward_grouped(x, out=ys[0])
+        L.forward_grouped(x, out=ys[1])
+    with torch.cuda.graph(graphs[1]):  # while the first has never run
+        L.forward_grouped(x, out=ys[2])
+    want = L.forward_grouped(x)  # and an eager call before either
+    torch.cuda.synchronize()
+    ref, _, tol = block_ref(x, L.w, 4)
+    close(want, ref, tol)
+    for g in (graphs[1], graphs[0], graphs[1]):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in ys)
+    L.check()
+
+
+def test_block_errors_survive_a_longer_call():
+    xs = tokens_of(40, 800)
+    L = small_layer()
+    L.forward_grouped(xs[0])
+    (ws,) = L._wsg.values()
+    ws[:4].view(torch.int32)[0] = 8  # as a bad plan records it
+    L.forward_grouped(xs[1])
+    with pytest.raises(M.MoeError, match="MOE_EDEVICE"):
+        L.check()
+    L.check()
+
+
+def test_decode_on_a_side_stream_first_and_longer():
+    L = M.Layer(synth.layer_weights(synth.TINY, seed=31), top_e=2)
+    L.build_sketch(synth.rot_seed(0)).build_lowrank(8)
+    xs = [synth.tokens(256, n, seed=n).cuda() for n in (1, 2, 5, 40)]
+    want = [(L.forward(x, k=24, c=48), L.forward_dense(x)) for x in xs]
+    L.check()
+    L._ws = None
+    s = torch.cuda.Stream()
+    leave_bytes(M.moe_reader_workspace_bytes(40, 8, 2, 128, 256, 1, 1, 8), s)
+    for x, (w, wd) in zip(xs, want):
+        torch.cuda.synchronize()
+        keep_busy()
+        y, yd = L.forward(x, k=24, c=48, stream=s), L.forward_dense(x, stream=s)
+        s.synchronize()
+        assert torch.equal(y, w) and torch.equal(yd, wd)
+    L.check()
