@@ -508,6 +508,14 @@ class Layer:
         with on:
             return self._scratch("_ws", self._reader_bytes(B), handle)
 
+    def block_workspace(self, B: int):
+        """A new workspace for forward_grouped of up to B tokens.  Layers of one
+        shape may use one in turn; calls that may overlap need one each."""
+        nb = moe_reader_block_workspace_bytes(B, self.E, self.top_e, self.I, self.d)
+        if nb == 0:
+            raise MoeError(MOE_EINVAL, f"no block of {B} tokens")
+        return torch.zeros(nb, dtype=torch.uint8, device=self.w["w_gate"].device)
+
     def _debug(self, B, k, c, dev):
         P = (B, self.top_e)
         dbg_t = dict(ids=torch.empty(P, dtype=torch.int32, device=dev),
@@ -567,11 +575,16 @@ class Layer:
             made.append(y)
         return y
 
-    def forward_grouped(self, x, residual=None, ids=None, stream=None, out=None):
+    def forward_grouped(self, x, residual=None, ids=None, stream=None, out=None, workspace=None):
         """The all-channel block over any number of tokens (prompts): x,
         residual and out [B, d] bf16; ids, if given, receives the chosen
-        experts ([B, top_e] int32). The layer
-        keeps a workspace for each stream it is called on."""
+        experts ([B, top_e] int32).
+
+        workspace: of block_workspace, or the layer's own (None), of which it
+        keeps one for each stream it is called on.  Pass one to let the layers
+        of a model share it, or where captured graphs of this layer may run at
+        the same time; it has to outlive the graphs, and its errors are read
+        by moe_reader_check_error."""
         B = x.shape[0]
         for name, t, shape in (("x", x, (B, self.d)), ("residual", residual, (B, self.d)), ("out", out, (B, self.d)),
                                ("ids", ids, (B, self.top_e))):
@@ -581,9 +594,9 @@ class Layer:
             raise MoeError(MOE_EINVAL, f"x is on {x.device}, the layer on {self.w['w_gate'].device}")
         nb = moe_reader_block_workspace_bytes(B, self.E, self.top_e, self.I, self.d)
         with torch.cuda.device(x.device):
-            handle, on = self._on(stream, x, residual, out, ids)
+            handle, on = self._on(stream, x, residual, out, ids, workspace)
             with on as made:
-                ws = self._scratch("_wsg", max(nb, 16), handle)
+                ws = workspace if workspace is not None else self._scratch("_wsg", max(nb, 16), handle)
                 y = out if out is not None else torch.empty_like(x)
                 moe_reader_forward_grouped(self.struct(0), B, x, residual, y, ids, ws, ws.nbytes, handle)
                 made.append(y)

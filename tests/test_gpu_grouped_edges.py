@@ -380,6 +380,24 @@ def test_captured_block_without_a_call_before():
     L.check()
 
 
+def test_layers_share_a_workspace_that_is_passed():
+    xs = tokens_of(40, 800)
+    layers = [small_layer(seed) for seed in (24, 25)]
+    want = [[L.forward_grouped(x) for x in xs] for L in layers]
+    fresh = [small_layer(seed) for seed in (24, 25)]
+    ws = fresh[0].block_workspace(800)
+    for _ in range(2):
+        for i, x in enumerate(xs):
+            for L, w in zip(fresh, want):
+                assert torch.equal(L.forward_grouped(x, workspace=ws), w[i])
+    M.moe_reader_check_error(ws)
+    assert not fresh[0]._wsg and not fresh[1]._wsg
+    with pytest.raises(M.MoeError, match="MOE_EINVAL.*workspace"):
+        fresh[0].forward_grouped(xs[1], workspace=fresh[0].block_workspace(40))
+    with pytest.raises(M.MoeError, match="MOE_EINVAL"):
+        fresh[0].block_workspace(32769)
+
+
 def test_block_errors_survive_a_longer_call():
     xs = tokens_of(40, 800)
     L = small_layer()
