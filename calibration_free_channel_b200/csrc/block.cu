@@ -22,9 +22,11 @@ constexpr int kExactTokens = 64;
 // products), which are off by at most
 //   delta = d 2^-23 |x| |w_e|  (2-norms)
 // and a sixteenth more (every partial sum is bounded by |x| |w_e|, and a step
-// of 16 products cuts 17 terms).  Experts whose fp32 logits are more than 2 delta apart are in the
+// of 16 products cuts 17 terms), and by 2^-125 for each product that may be
+// too small for a normal number.  Experts whose fp32 logits are more than 2 delta apart are in the
 // right order; the others near or above the last chosen place are computed
-// again in fp64, and the order of the candidates is decided by that.
+// again in fp64, and the order of the candidates is decided by that.  Where a
+// sum may leave the range of fp32, all of a token's are.
 __device__ __forceinline__ void dot64x2(const uint16_t* x, const uint16_t* w0, const uint16_t* w1, int d, int lane,
                                         double& s0, double& s1) {
   s0 = s1 = 0.0;
@@ -34,11 +36,12 @@ __device__ __forceinline__ void dot64x2(const uint16_t* x, const uint16_t* w0, c
                 c = *reinterpret_cast<const uint4*>(w1 + k);
     const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w}, cv[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int i = 0; i < 4; i++) {  // products of two bf16 are exact in fp32
-      s0 += (double)(bf16lo(av[i]) * bf16lo(bv[i]));
-      s0 += (double)(bf16hi(av[i]) * bf16hi(bv[i]));
-      s1 += (double)(bf16lo(av[i]) * bf16lo(cv[i]));
-      s1 += (double)(bf16hi(av[i]) * bf16hi(cv[i]));
+    for (int i = 0; i < 4; i++) {  // products of two bf16 are exact in fp64 (in fp32 the smallest and largest are not)
+      const double lo = bf16lo(av[i]), hi = bf16hi(av[i]);
+      s0 = fma(lo, (double)bf16lo(bv[i]), s0);
+      s0 = fma(hi, (double)bf16hi(bv[i]), s0);
+      s1 = fma(lo, (double)bf16lo(cv[i]), s1);
+      s1 = fma(hi, (double)bf16hi(cv[i]), s1);
     }
   }
   s0 = warp_sum(s0);
@@ -51,6 +54,8 @@ __device__ __forceinline__ V ranked(V v) {
   return v == v ? v : (V)-INFINITY;
 }
 
+// An upper bound of the 2-norm: fp32 sums are off by less than a thousandth
+// unless squares leave the range, and are summed in fp64 then.
 __device__ __forceinline__ float norm2(const uint16_t* x, int d, int lane) {
   float s = 0.0f;
 #pragma unroll 4
@@ -63,7 +68,14 @@ __device__ __forceinline__ float norm2(const uint16_t* x, int d, int lane) {
       s = fmaf(bf16hi(av[i]), bf16hi(av[i]), s);
     }
   }
-  return sqrtf(warp_sum(s)) * 1.001f;  // an upper bound: the fp32 sum is off by less
+  s = warp_sum(s);
+  if (s > 0x1p-60f && s < 0x1p120f) return sqrtf(s) * 1.001f;
+  double t = 0.0;
+  for (int k = lane; k < d; k += 32) {
+    const double v = bf16f(x[k]);
+    t = fma(v, v, t);
+  }
+  return __double2float_ru(sqrt(warp_sum(t)) * 1.001);
 }
 
 __global__ void __launch_bounds__(256) norms_kernel(BlockArgs a) {
@@ -191,12 +203,14 @@ __global__ void __launch_bounds__(256) choose_kernel(BlockArgs a) {
     l_max = fmaxf(l_max, __shfl_xor_sync(0xffffffffu, l_max, o));
   }
   // the sum's error, and the bias's addition
-  const float apart = 2.0f * (1.0625f * (float)a.d * 0x1p-23f * norm2(x, a.d, lane) * w_max + 0x1p-23f * l_max);
+  const float most = norm2(x, a.d, lane) * w_max;
+  const float apart = 2.0f * (1.0625f * (float)a.d * (0x1p-23f * most + 0x1p-125f) + 0x1p-23f * l_max);
+  const bool in_range = most < 0x1p126f && l_max < 0x1p126f;
   // the chosen by these logits, in order, one to a lane, and behind them
   // those within reach of the last
   float mine = 0.0f, last = 0.0f;
   int n = 0;
-  for (; n < 32 && n < a.E; n++) {
+  for (; in_range && n < 32 && n < a.E; n++) {
     float best;
     int e;
     largest(v, a.E, lane, taken, best, e);
@@ -207,8 +221,8 @@ __global__ void __launch_bounds__(256) choose_kernel(BlockArgs a) {
       id = e;
     }
   }
-  if (n == 32 && a.E > 32) {
-    // too many within reach (equal rows, a token of zeros): all of them in fp64
+  if (!in_range || (n == 32 && a.E > 32)) {
+    // out of range, or too many within reach (equal rows, a token of zeros): all of them in fp64
     double all[kM], got = 0.0;
 #pragma unroll
     for (int m = 0; m < kM; m++) {

@@ -426,3 +426,60 @@ def test_decode_on_a_side_stream_first_and_longer():
         s.synchronize()
         assert torch.equal(y, w) and torch.equal(yd, wd)
     L.check()
+
+
+# ------------------------------------------------------------------- routing
+def chosen(L, x, top, **kw):
+    ids = torch.full((x.shape[0], top), -1, dtype=torch.int32, device="cuda")
+    L.forward_grouped(x, ids=ids)
+    L.check()
+    logits = x.double() @ L.w["w_router"].double().T
+    if L.w["router_bias"] is not None:
+        logits = logits + L.w["router_bias"].double()
+    return ids.long(), torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :top]
+
+
+@pytest.mark.parametrize("E", [16, 40])
+@pytest.mark.parametrize("scale", [2.0 ** -125, 2.0 ** -100, 2.0 ** -70, 2.0 ** -20, 2.0 ** 30, 2.0 ** 90, 2.0 ** 121])
+def test_block_near_ties_of_tokens_of_any_size(scale, E):
+    """Router rows a bf16 step of one weight apart, and tokens whose squares
+    (or products) leave the range of fp32: the order is still that of 64 bits."""
+    W = synth.layer_weights(synth.BlockShape(E, 16, 2048, 3), seed=12, device="cuda")
+    r = W["w_router"]
+    r[9], r[1] = r[4], r[4]
+    r[9, 100] = r[4, 100] + 2.0 ** -14
+    r[1, 900] = r[4, 900] - 2.0 ** -14
+    L = M.Layer(W, top_e=3)
+    x = synth.tokens(2048, 1500, seed=13).cuda()
+    x[:, 100] = dev(1500, seed=1, scale=1e-3)
+    x[:, 900] = dev(1500, seed=2, scale=1e-3)
+    x[7] = 0
+    got, want = chosen(L, (x.float() * scale).bfloat16(), 3)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("B", [10, 100])
+def test_block_products_below_fp32_decide(B):
+    W = one_expert(E=8)
+    W["w_router"][:, 5] = torch.arange(1, 9).cuda() * 2.0 ** -78
+    L = M.Layer(W, top_e=2)
+    x = torch.zeros((B, 256), dtype=torch.bfloat16, device="cuda")
+    x[:, 5] = 2.0 ** -80
+    x[3::5, 5] = -2.0 ** -80
+    got, want = chosen(L, x, 2)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("E", [16, 40])
+@pytest.mark.parametrize("mask", [float("-inf"), -3.38e38])
+def test_block_masked_experts(E, mask):
+    """A bias that takes experts out: none of them is chosen while others are left, and the rest keeps its order."""
+    W = synth.layer_weights(synth.BlockShape(E, 16, 256, 3), seed=14, bias=True, device="cuda")
+    W["router_bias"][::2] = mask
+    L = M.Layer(W, top_e=3)
+    x = synth.tokens(256, 200, seed=15).cuda()
+    got, want = chosen(L, x, 3)
+    assert torch.equal(got, want) and bool((got % 2 == 1).all())
+    W["router_bias"][3:] = mask  # one expert left
+    got, want = chosen(M.Layer(W, top_e=3), x, 3)
+    assert torch.equal(got, want) and bool((got[:, 0] == 1).all())
