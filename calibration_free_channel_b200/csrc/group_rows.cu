@@ -35,8 +35,9 @@ cudaError_t launch_group_rows(int n, int n_groups, const int32_t* ids, int32_t* 
   cfg.blockDim = dim3(1024);
   cfg.dynamicSmemBytes = sort_bytes(n, n_groups, stretch);
   if (cfg.dynamicSmemBytes > 48 * 1024) {
-    cudaError_t e =
-        cudaFuncSetAttribute(group_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    // the most of any call, so that calls of other threads never lower it
+    const int most = (int)sort_bytes(kMaxRows, kMaxGroups, sort_stretch(kMaxRows, kSortCtas));
+    cudaError_t e = cudaFuncSetAttribute(group_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }
   cfg.stream = s;

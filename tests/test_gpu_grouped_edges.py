@@ -1,6 +1,8 @@
 """The products over ragged groups where values or calls are out of the
 ordinary: ranges, non-finite weights, streams and captures, both sides of the
 borders between kernels.  Tolerances as in test_gpu_grouped.py."""
+import threading
+
 import pytest
 import torch
 
@@ -483,3 +485,35 @@ def test_block_masked_experts(E, mask):
     W["router_bias"][3:] = mask  # one expert left
     got, want = chosen(M.Layer(W, top_e=3), x, 3)
     assert torch.equal(got, want) and bool((got[:, 0] == 1).all())
+
+
+# ------------------------------------------------------------------- threads
+def test_plans_of_several_threads():
+    """Calls of very different table sizes at once, a stream each: a launch never finds its shared memory taken back."""
+    sizes = [(65536, 1024), (20000, 400), (3000, 1000), (40000, 700)]
+    found = []
+
+    def run(n, G, seed):
+        try:
+            ids = torch.randint(-1, G, (n,), generator=torch.Generator("cuda").manual_seed(seed), device="cuda",
+                                dtype=torch.int32)
+            key = torch.where(ids < 0, G, ids)
+            want = torch.sort(key, stable=True).indices.int()
+            off, rows = torch.empty(G + 1, dtype=torch.int32, device="cuda"), torch.empty(n, dtype=torch.int32, device="cuda")
+            ws = ws_for(M.moe_reader_group_workspace_bytes(n, G))
+            s = torch.cuda.Stream()
+            torch.cuda.synchronize()
+            for _ in range(400):
+                M.moe_reader_group_rows(n, G, ids, off, rows, ws, ws.numel(), stream=s)
+            s.synchronize()
+            if not torch.equal(rows, want):
+                found.append((n, G, "rows"))
+        except Exception as e:  # noqa: BLE001 (shown below)
+            found.append((n, G, e))
+
+    threads = [threading.Thread(target=run, args=(n, G, i)) for i, (n, G) in enumerate(sizes)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not found, found
