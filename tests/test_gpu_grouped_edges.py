@@ -517,3 +517,68 @@ def test_plans_of_several_threads():
     for t in threads:
         t.join()
     assert not found, found
+
+
+# ------------------------------------------- SwiGLU values between the products
+def held_ref(x, w, top, held):
+    """The block in 64 bits, and its tolerance with SwiGLU values that are off by `held` of themselves."""
+    y, ids, _ = block_ref(x, w, top)
+    xd, err = x.double(), torch.zeros_like(y)
+    logits = xd @ w["w_router"].double().T
+    if w["router_bias"] is not None:
+        logits = logits + w["router_bias"].double()
+    share = torch.softmax(torch.sort(logits, dim=1, descending=True, stable=True).values[:, :top], 1)
+    for e in range(logits.shape[1]):
+        t, k = (ids == e).nonzero(as_tuple=True)
+        a, ea = swiglu_ref(xd[t], w["w_gate"][e], w["w_up"][e])
+        wd = w["w_down"][e].double().abs()
+        err[t] += share[t, k][:, None] * ((ea + (held + sum_err(2 * a.shape[1] + 16)) * a.abs()) @ wd)
+    # the routing weights: logits in fp32 (d 2^-23 of the terms' sizes) and their exponentials
+    err += (2 * sum_err(x.shape[1]) * xd.norm(dim=1) * w["w_router"].double().norm(dim=1).max())[:, None] * y.abs()
+    return y, ids, HALF * y.abs() + SLACK * (err + 2.0 ** -20 * y.abs())
+
+
+@pytest.mark.parametrize("E,top,B", [(8, 2, 1), (8, 2, 64), (8, 2, 65), (8, 2, 256), (1, 1, 64), (4, 4, 64), (16, 1, 1024),
+                                     (8, 2, 257), (1, 1, 65), (16, 1, 1025)])
+def test_block_holds_swiglu_in_two_terms_up_to_its_border(E, top, B):
+    """Up to B top_e = 64 E the values keep 16 bits, above that 8."""
+    d, I = 256, 128
+    W = synth.layer_weights(synth.BlockShape(E, I, d, top), seed=50, device="cuda")
+    L = M.Layer(W, top_e=top)
+    x = synth.tokens(d, B, seed=51).cuda()
+    y = L.forward_grouped(x)
+    L.check()
+    ref, _, tol = held_ref(x, L.w, top, 2.0 ** -16 if B * top <= 64 * E else HALF)
+    close(y, ref, tol)
+
+
+@pytest.mark.parametrize("E,B", [(1, 1), (1, 40), (1, 64), (4, 65), (4, 200), (4, 256), (40, 2000)])
+def test_block_second_term_decides_where_the_first_cancels(E, B):
+    """Pairs of channels that differ by 2^-10 of themselves and are subtracted:
+    one bf16 term would leave nothing, or four times as much."""
+    d, I = 256, 64
+    W = one_expert(d, I, E)
+    x = torch.zeros((B, d), dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1.0 + torch.arange(B, device="cuda").bfloat16() / 64  # gates
+    x[:, 1] = 1.0 + dev(B, seed=52).abs()
+    x[:, 2] = x[:, 1] * 2.0 ** -10
+    x[:, 3 + torch.arange(E, device="cuda")] = 0.0
+    x[torch.arange(B, device="cuda"), 3 + torch.arange(B, device="cuda") % E] = 8.0  # the token's expert
+    for e in range(E):
+        W["w_router"][e, 3 + e] = 1.0
+    W["w_gate"][:, :, 0] = 1.0
+    W["w_up"][:, :, 1] = 1.0
+    W["w_up"][:, 1::2, 2] = 1.0
+    for c in range(I // 2):
+        W["w_down"][:, 2 * c, c::32] = -1.0
+        W["w_down"][:, 2 * c + 1, c::32] = 1.0
+    L = M.Layer(W, top_e=1)
+    y = L.forward_grouped(x)
+    L.check()
+    xd = x.double()
+    silu = xd[:, 0] * torch.sigmoid(xd[:, 0])
+    ref = (silu * xd[:, 2])[:, None].expand(B, d)
+    # two values of 16 bits each, their fp32 arithmetic a few 2^-24
+    tol = HALF * ref + 2 * (2.0 ** -16 + 2.0 ** -20) * (silu * xd[:, 1])[:, None]
+    close(y, ref, tol)
+    assert bool((tol < ref / 4).all())
