@@ -582,3 +582,123 @@ def test_block_second_term_decides_where_the_first_cancels(E, B):
     tol = HALF * ref + 2 * (2.0 ** -16 + 2.0 ** -20) * (silu * xd[:, 1])[:, None]
     close(y, ref, tol)
     assert bool((tol < ref / 4).all())
+
+
+# --------------------------- adapters on both sides of z's border (2048 tokens)
+BORDER = [2048, 2049, 2500]
+
+
+def adapter_ids(T, A, kind, seed=0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    rnd = lambda: torch.randint(-1, A, (T,), generator=g, device="cuda", dtype=torch.int32)
+    if kind == "runs":
+        return rnd().repeat_interleave(37)[:T].contiguous()
+    return {"random": rnd, "all": lambda: torch.zeros(T, dtype=torch.int32, device="cuda"),
+            "none": lambda: torch.full((T,), -1, dtype=torch.int32, device="cuda"),
+            "distinct": lambda: torch.arange(T, device="cuda", dtype=torch.int32) % A,
+            "one of many": lambda: torch.where(torch.arange(T, device="cuda") == T // 2, A - 1, -1).int()}[kind]()
+
+
+@pytest.mark.parametrize("T", BORDER)
+@pytest.mark.parametrize("r", [8, 72, 128])
+@pytest.mark.parametrize("K", [8, 200])
+def test_adapters_at_the_border_ranks(T, r, K):
+    for A, kind, w, base, scale in ((3, "random", True, False, {}), (4, "runs", False, True, dict(scale=None))):
+        y, ids, t = adapter_call(T, A, K, 136, r, use_w=w, use_base=base, ids=adapter_ids(T, A, kind), **scale)
+        close(y, *adapter_ref(t, ids, 136))
+
+
+@pytest.mark.parametrize("T", BORDER)
+@pytest.mark.parametrize("A,kind", [(1, "all"), (1, "none"), (300, "distinct"), (300, "random"), (1024, "distinct"),
+                                    (1024, "one of many"), (40, "runs")])
+def test_adapters_at_the_border_counts(T, A, kind):
+    for w, base in ((True, True), (False, False)):
+        y, ids, t = adapter_call(T, A, 136, 264, 24, use_w=w, use_base=base, ids=adapter_ids(T, A, kind))
+        close(y, *adapter_ref(t, ids, 264))
+
+
+@pytest.mark.parametrize("T", BORDER)
+def test_adapters_at_the_border_in_place(T):
+    a, ids, t = adapter_call(T, 7, 256, 520, 16, use_w=False)
+    b, _, _ = adapter_call(T, 7, 256, 520, 16, use_w=False, inplace=True)
+    assert torch.equal(a, b)
+    close(a, *adapter_ref(t, ids, 520))
+
+
+@pytest.mark.parametrize("T", BORDER)
+def test_adapters_at_the_border_nonfinite_tokens(T):
+    y, ids, t = adapter_call(T, 6, 128, 264, 24)
+    x = t["x"].clone()
+    x[11], x[T - 1], x[700, 5] = float("nan"), float("inf"), float("nan")
+    z, _, _ = adapter_call(T, 6, 128, 264, 24, x=x)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[[11, T - 1, 700]] = False
+    assert torch.equal(z[keep], y[keep])
+    assert not bool(torch.isfinite(z[[11, 700]]).any())
+
+
+@pytest.mark.parametrize("T", BORDER)
+@pytest.mark.parametrize("where", [0, 700, -1])
+@pytest.mark.parametrize("bad", [-1, "T", 2 ** 31 - 1, -2 ** 31])
+def test_adapters_at_the_border_bad_rows(T, where, bad):
+    A, K, N, r = 4, 64, 72, 8
+    y, ids, t = adapter_call(T, A, K, N, r)
+    off, rows = torch.empty(A + 1, dtype=torch.int32, device="cuda"), torch.empty(T, dtype=torch.int32, device="cuda")
+    ws = ws_for(M.moe_reader_adapter_workspace_bytes(T, A, K, N, r))
+    M.moe_reader_group_rows(T, A, ids, off, rows, ws, ws.numel())
+    lost = int(rows[where])
+    rows[where] = T if bad == "T" else bad
+    z = torch.full((T, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    M.moe_reader_adapter_product(T, A, N, K, r, t["x"], t["w"], t["base"], off, rows, t["a"], t["b"], t["scale"], z, ws,
+                                 ws.numel())
+    with pytest.raises(M.MoeError, match="MOE_EDEVICE"):
+        M.moe_reader_check_error(ws)
+    keep = torch.arange(T, device="cuda") != lost
+    assert torch.equal(z[keep], y[keep]) and bool((z[lost] == 9.0).all())
+
+
+@pytest.mark.parametrize("T", BORDER)
+@pytest.mark.parametrize("off", [[0, 5, 4, 20], [-1, 5, 10, 20], [0, 5, 10, 5000], [0, 2 ** 31 - 1, -2 ** 31, 20]])
+def test_adapters_at_the_border_bad_offsets(T, off):
+    A, K, N, r = 3, 64, 72, 8
+    off = torch.tensor(off, dtype=torch.int32, device="cuda")
+    rows = torch.arange(T, dtype=torch.int32, device="cuda")
+    ws = ws_for(M.moe_reader_adapter_workspace_bytes(T, A, K, N, r))
+    y = torch.full((T + 1, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    M.moe_reader_adapter_product(T, A, N, K, r, dev(T, K, seed=1), dev(N, K, seed=2), None, off, rows,
+                                 dev(A, r, K, seed=3), dev(A, N, r, seed=4), None, y, ws, ws.numel())
+    with pytest.raises(M.MoeError, match="MOE_EDEVICE"):
+        M.moe_reader_check_error(ws)
+    M.moe_reader_check_error(ws)
+    assert bool((y[T] == 9.0).all())
+
+
+@pytest.mark.parametrize("T", BORDER)
+def test_adapters_at_the_border_captured(T):
+    A, K, N, r = 6, 264, 520, 24
+    x, w, base = dev(T, K, seed=80), dev(N, K, seed=81, scale=K ** -0.5), dev(T, N, seed=82)
+    a, b = dev(A, r, K, seed=83, scale=K ** -0.5), dev(A, N, r, seed=84)
+    ids = adapter_ids(T, A, "random")
+    off, rows = torch.zeros(A + 1, dtype=torch.int32, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    ws = ws_for(M.moe_reader_adapter_workspace_bytes(T, A, K, N, r))
+
+    def step():
+        M.moe_reader_group_rows(T, A, ids, off, rows, ws, ws.numel())
+        M.moe_reader_adapter_product(T, A, N, K, r, x, w, base, off, rows, a, b, None, y, ws, ws.numel())
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for k, kind in enumerate(("random", "none", "runs", "all")):
+        ids.copy_(adapter_ids(T, A, kind, seed=k))
+        x.copy_(dev(T, K, seed=90 + k))
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        step()
+        assert torch.equal(got, y)
+        close(got, *adapter_ref(dict(x=x, w=w, base=base, a=a, b=b, scale=None), ids, N))
+    M.moe_reader_check_error(ws)
