@@ -194,7 +194,9 @@ __global__ void __launch_bounds__(256) choose_kernel(BlockArgs a) {
       const float l = a.approx[(size_t)t * a.E + e], b = a.bias ? a.bias[e] : 0.0f;
       v[m] = ranked(l + b);
       w_max = fmaxf(w_max, a.w_norm[e]);
-      l_max = fmaxf(l_max, fabsf(l) + fabsf(b));
+      // (a bias of -infinity takes an expert out, in any precision: with it here
+      // every logit would be summed in fp64, 8192 tokens 1534 instead of 851 us)
+      if (v[m] > -INFINITY) l_max = fmaxf(l_max, fabsf(l) + fabsf(b));
     }
   }
 #pragma unroll
