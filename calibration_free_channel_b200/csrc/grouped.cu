@@ -27,7 +27,7 @@
 // further stages: A is B_g, B the rows of z = scale x A_g^T (adapter.cu), the
 // accumulator's columns those of the adapter, widened to multiples of 32 with
 // zero rows.  So the low-rank term costs its own bytes and products only.
-// For many tokens z itself comes from these tiles (kLowRank: W_g = A_g, and a
+// For many values of z it comes from these tiles (kLowRank: W_g = A_g, and a
 // group's range of positions widened as z's is).
 //
 // A call with few tiles splits their sums over K: each part is written in
@@ -78,10 +78,17 @@ constexpr int kABytes = kLanes * kBlockK * 2;
 constexpr int kMaxStages = 8;
 constexpr int kMaxPairs = 74;              // CTA pairs of a launch
 constexpr int kMaxSplit = 8;               // parts of a tile's sum
-// Up to here z comes from adapter.cu (8 adapters, rank 64, 2048 x 2048, whole
-// call: 512 tokens 29.7 us against 37.0 with z's tiles, 2048 42.7 against
-// 44.7; 4100 tokens beside 4096 channels 119 against 101).
-constexpr int kFewTokens = 2048;
+// Where z comes from: adapter.cu takes 16 rows at a time and reads A_g again
+// for each, so its time goes with T r K and it leaves the tiles that follow
+// less shared memory; z's tiles cost the same at any rank, and a wave of their
+// own.  Whole calls, adapter.cu against tiles: rank 64, K = N = 2048, 8
+// adapters, 2048 tokens 35.4 against 46.1 us, 3000 49.2 against 47.2, 8000 110
+// against 91; rank 16 4100 tokens 45.9 against 60.2, 8000 81.7 against 91.9;
+// rank 128 2048 tokens 41.3 against 46.3.  K = 4096 beside 4096 channels, rank
+// 16, 2500 tokens 116 against 103, 4100 146 against 160, 8000 240 against 231.
+bool few_values(long T, int r, int K) {
+  return T <= 2048 || (T * r <= 2048 * 64 && K <= 2048);
+}
 // Stages of K that a part has at least (one token, 2048 x 2048: 12.8 us at 8,
 // 13.2 at 4, 17.8 without parts; K = 512: 10.3 without, 11.1 with two).
 constexpr int kMinPart = 8;
@@ -909,9 +916,9 @@ cudaError_t run_tiles(const Maps& m, TileArgs t, cudaStream_t s) {
   // (32 at least: an adapter's narrowest columns with both halves of z)
   t.b_rows = t.two_terms ? t.cols : t.cols / 2 < 32 ? 32 : t.cols / 2;
   t.stage_bytes = kABytes + t.b_rows * 128;
-  // Beside the launch of z for few tokens, whose CTAs take up to 73 KB, a pair
+  // Beside the launch of z in adapter.cu, whose CTAs take up to 73 KB, a pair
   // finds room only if it takes the rest at most; it starts 5 us later otherwise.
-  const int budget = kMode == kAdapter && t.P <= kFewTokens ? kSmemBudget - 74 * 1024 : kSmemBudget;
+  const int budget = kMode == kAdapter && few_values(t.P, t.r, t.K) ? kSmemBudget - 74 * 1024 : kSmemBudget;
   t.stages = (budget - side_bytes<kMode>()) / t.stage_bytes;
   if (t.stages > kMaxStages) t.stages = kMaxStages;
   t.max_split = kMode == kLowRank ? 1 : kMaxSplit;
@@ -1021,8 +1028,8 @@ cudaError_t launch_grouped(const GroupedArgs& a, cudaStream_t s) {
 
 cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s) {
   const uint64_t N = a.N, K = a.K, r = a.r, zr = adapter_z_rows(a.T, a.A);
-  // z on the tensor cores, for many tokens
-  const bool many = a.T > kFewTokens;
+  // z on the tensor cores
+  const bool many = !few_values(a.T, a.r, a.K);
   TileArgs z = {};
   Maps mz;
   if (many) {

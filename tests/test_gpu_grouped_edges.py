@@ -57,10 +57,11 @@ def adapter_call(T, A, K, N, r, seed=0, use_w=True, use_base=True, ids=None, inp
 
 
 @pytest.mark.parametrize("T,A", [(3, 2), (90, 5), (700, 40), (2100, 5), (2300, 60)])
+@pytest.mark.parametrize("r", [24, 64])
 @pytest.mark.parametrize("bad", ["a nan", "a inf", "scale"])
-def test_adapters_down_side_nonfinite_stays_apart(T, A, bad):
+def test_adapters_down_side_nonfinite_stays_apart(T, A, r, bad):
     """Weights of A or a scale that are not finite reach the adapter's own tokens only."""
-    K, N, r = 256, 264, 24
+    K, N = 256, 264
     y, ids, t = adapter_call(T, A, K, N, r)
     a, scale = t["a"].clone(), t["scale"].clone()
     if bad == "scale":
@@ -99,11 +100,12 @@ def adapter_ref(t, ids, N):
 
 
 @pytest.mark.parametrize("T,A", [(2, 2), (3, 2), (64, 32), (90, 5), (700, 40), (2100, 5), (2300, 60)])
+@pytest.mark.parametrize("r", [24, 64])
 @pytest.mark.parametrize("use_w,use_base,inplace", [(True, False, False), (False, True, True), (True, True, False)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_adapters_up_side_nonfinite_stays_apart(T, A, use_w, use_base, inplace, bad):
+def test_adapters_up_side_nonfinite_stays_apart(T, A, r, use_w, use_base, inplace, bad):
     """Weights of B that are not finite reach the adapter's own tokens only, in the channels that have them."""
-    K, N, r = 264, 520, 24
+    K, N = 264, 520
     y, ids, t = adapter_call(T, A, K, N, r, use_w=use_w, use_base=use_base)
     b = t["b"].clone()
     b[1, 0, 3] = b[1, 77, 0] = b[1, 78, 23] = b[1, 519, 8] = bad
@@ -177,7 +179,7 @@ def test_adapters_infinite_results_stay():
 @pytest.mark.parametrize("T", [5, 100, 2100])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 def test_adapters_two_terms_below_overflow(T, sign):
-    K, N, r = 64, 64, 8
+    K, N, r = 64, 64, 64
     x = torch.zeros((T, K), dtype=torch.bfloat16, device="cuda")
     a = torch.zeros((1, r, K), dtype=torch.bfloat16, device="cuda")
     x[:, 0], x[:, 1] = sign * 255 * 2.0 ** 57, sign * 1.5 * 2.0 ** 60
@@ -584,8 +586,14 @@ def test_block_second_term_decides_where_the_first_cancels(E, B):
     assert bool((tol < ref / 4).all())
 
 
-# --------------------------- adapters on both sides of z's border (2048 tokens)
-BORDER = [2048, 2049, 2500]
+# ------------------------ adapters on both sides of z's border (2048 tokens, more of rank below 64)
+def border(r):
+    """Tokens up to, and from, which z of rank r comes from another kernel."""
+    most = max(2048, 2048 * 64 // r)
+    return [most, most + 1, most + 450]
+
+
+SIDES = [0, 1, 2]
 
 
 def adapter_ids(T, A, kind, seed=0):
@@ -599,49 +607,54 @@ def adapter_ids(T, A, kind, seed=0):
             "one of many": lambda: torch.where(torch.arange(T, device="cuda") == T // 2, A - 1, -1).int()}[kind]()
 
 
-@pytest.mark.parametrize("T", BORDER)
+@pytest.mark.parametrize("side", SIDES)
 @pytest.mark.parametrize("r", [8, 72, 128])
 @pytest.mark.parametrize("K", [8, 200])
-def test_adapters_at_the_border_ranks(T, r, K):
+def test_adapters_at_the_border_ranks(side, r, K):
+    T = border(r)[side]
     for A, kind, w, base, scale in ((3, "random", True, False, {}), (4, "runs", False, True, dict(scale=None))):
         y, ids, t = adapter_call(T, A, K, 136, r, use_w=w, use_base=base, ids=adapter_ids(T, A, kind), **scale)
         close(y, *adapter_ref(t, ids, 136))
 
 
-@pytest.mark.parametrize("T", BORDER)
+@pytest.mark.parametrize("side", SIDES)
 @pytest.mark.parametrize("A,kind", [(1, "all"), (1, "none"), (300, "distinct"), (300, "random"), (1024, "distinct"),
                                     (1024, "one of many"), (40, "runs")])
-def test_adapters_at_the_border_counts(T, A, kind):
+def test_adapters_at_the_border_counts(side, A, kind):
+    T = border(64)[side]
     for w, base in ((True, True), (False, False)):
-        y, ids, t = adapter_call(T, A, 136, 264, 24, use_w=w, use_base=base, ids=adapter_ids(T, A, kind))
+        y, ids, t = adapter_call(T, A, 136, 264, 64, use_w=w, use_base=base, ids=adapter_ids(T, A, kind))
         close(y, *adapter_ref(t, ids, 264))
 
 
-@pytest.mark.parametrize("T", BORDER)
-def test_adapters_at_the_border_in_place(T):
-    a, ids, t = adapter_call(T, 7, 256, 520, 16, use_w=False)
-    b, _, _ = adapter_call(T, 7, 256, 520, 16, use_w=False, inplace=True)
+@pytest.mark.parametrize("side", SIDES)
+def test_adapters_at_the_border_in_place(side):
+    T = border(64)[side]
+    a, ids, t = adapter_call(T, 7, 256, 520, 64, use_w=False)
+    b, _, _ = adapter_call(T, 7, 256, 520, 64, use_w=False, inplace=True)
     assert torch.equal(a, b)
     close(a, *adapter_ref(t, ids, 520))
 
 
-@pytest.mark.parametrize("T", BORDER)
-def test_adapters_at_the_border_nonfinite_tokens(T):
-    y, ids, t = adapter_call(T, 6, 128, 264, 24)
+@pytest.mark.parametrize("side", SIDES)
+def test_adapters_at_the_border_nonfinite_tokens(side):
+    T = border(72)[side]
+    y, ids, t = adapter_call(T, 6, 128, 264, 72)
     x = t["x"].clone()
     x[11], x[T - 1], x[700, 5] = float("nan"), float("inf"), float("nan")
-    z, _, _ = adapter_call(T, 6, 128, 264, 24, x=x)
+    z, _, _ = adapter_call(T, 6, 128, 264, 72, x=x)
     keep = torch.ones(T, dtype=torch.bool, device="cuda")
     keep[[11, T - 1, 700]] = False
     assert torch.equal(z[keep], y[keep])
     assert not bool(torch.isfinite(z[[11, 700]]).any())
 
 
-@pytest.mark.parametrize("T", BORDER)
+@pytest.mark.parametrize("side", SIDES)
 @pytest.mark.parametrize("where", [0, 700, -1])
 @pytest.mark.parametrize("bad", [-1, "T", 2 ** 31 - 1, -2 ** 31])
-def test_adapters_at_the_border_bad_rows(T, where, bad):
-    A, K, N, r = 4, 64, 72, 8
+def test_adapters_at_the_border_bad_rows(side, where, bad):
+    A, K, N, r = 4, 64, 72, 64
+    T = border(r)[side]
     y, ids, t = adapter_call(T, A, K, N, r)
     off, rows = torch.empty(A + 1, dtype=torch.int32, device="cuda"), torch.empty(T, dtype=torch.int32, device="cuda")
     ws = ws_for(M.moe_reader_adapter_workspace_bytes(T, A, K, N, r))
@@ -657,10 +670,11 @@ def test_adapters_at_the_border_bad_rows(T, where, bad):
     assert torch.equal(z[keep], y[keep]) and bool((z[lost] == 9.0).all())
 
 
-@pytest.mark.parametrize("T", BORDER)
+@pytest.mark.parametrize("side", SIDES)
 @pytest.mark.parametrize("off", [[0, 5, 4, 20], [-1, 5, 10, 20], [0, 5, 10, 5000], [0, 2 ** 31 - 1, -2 ** 31, 20]])
-def test_adapters_at_the_border_bad_offsets(T, off):
-    A, K, N, r = 3, 64, 72, 8
+def test_adapters_at_the_border_bad_offsets(side, off):
+    A, K, N, r = 3, 64, 72, 64
+    T = border(r)[side]
     off = torch.tensor(off, dtype=torch.int32, device="cuda")
     rows = torch.arange(T, dtype=torch.int32, device="cuda")
     ws = ws_for(M.moe_reader_adapter_workspace_bytes(T, A, K, N, r))
@@ -673,9 +687,10 @@ def test_adapters_at_the_border_bad_offsets(T, off):
     assert bool((y[T] == 9.0).all())
 
 
-@pytest.mark.parametrize("T", BORDER)
-def test_adapters_at_the_border_captured(T):
-    A, K, N, r = 6, 264, 520, 24
+@pytest.mark.parametrize("side", SIDES)
+def test_adapters_at_the_border_captured(side):
+    A, K, N, r = 6, 264, 520, 64
+    T = border(r)[side]
     x, w, base = dev(T, K, seed=80), dev(N, K, seed=81, scale=K ** -0.5), dev(T, N, seed=82)
     a, b = dev(A, r, K, seed=83, scale=K ** -0.5), dev(A, N, r, seed=84)
     ids = adapter_ids(T, A, "random")
