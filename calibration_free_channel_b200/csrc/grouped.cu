@@ -35,9 +35,9 @@
 //
 // What bounds it: few rows a group, the weights' bytes (128 experts of 768 x
 // 2048, gate and up, 4 rows each: 134 us, 6.0 TB/s); many, the stages' way
-// through a ring that holds 192 KB a CTA (512 rows each: 345 us, 1190 TFLOP/s,
-// as much as a batched library product of the same shape; 380 us gathered),
-// and in a row of calls the power limit (about 1.0 GHz at 990 W).  Copies of
+// through a ring that holds 192 KB a CTA (512 rows each: 340 us, 1214 TFLOP/s,
+// where a batched library product of the same shape, without the SwiGLU, takes
+// 314; 388 us gathered), and in a row of calls the power limit (about 1.0 GHz at 990 W).  Copies of
 // the weights into L2 ahead of the ring made every size slower, since they
 // cost the copy engine as much as the copies themselves; so did tiles sorted by
 // size, for few rows by more than the better balance gave for many.

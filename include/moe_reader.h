@@ -372,7 +372,8 @@ moe_status moe_reader_grouped_swiglu(int n_groups, int n_rows, int n_x, int I, i
  * w_layout 0: w is [n_groups, N, K] (row = output channel, as w_gate);
  * w_layout 1: w is [n_groups, K, N] (channel-major, as w_down).  x [n_x, K],
  * y [n_y, N] bf16; 1 <= n_x, n_y <= 1048576.  Rows of y that no position
- * names are left as they were; a row of y named twice gets one of the two. */
+ * names are left as they were; a row of y named twice gets, channel by channel,
+ * one of the two results (the one exception to the same bits on every call). */
 moe_status moe_reader_grouped_product(int n_groups, int n_rows, int n_x, int n_y, int N, int K, int w_layout,
                                       const uint16_t* x, const int32_t* x_rows, int x_div, const int32_t* offsets,
                                       const uint16_t* w, uint16_t* y, const int32_t* y_rows, void* workspace,
@@ -406,7 +407,10 @@ moe_status moe_reader_adapter_product(int T, int n_adapters, int N, int K, int r
  * the two grouped products; the pairs' outputs are summed with their routing
  * weights in fp32, slot order, `residual` (may be NULL, may be y) added, one
  * rounding.  Between the products the SwiGLU values are held in two bf16
- * terms (16 significant bits) while B top_e <= 64 E, and in one above.
+ * terms (16 significant bits) while B top_e <= 64 E, and in one above (the
+ * result's error against 64 bits is 0.0017 of it, and 0.0023 above).  Which
+ * experts are chosen, and their order, is decided in fp64; above 64 tokens the
+ * weights come from logits summed in fp32 where no other logit is near.
  * ids: DEVICE [B, top_e] int32, receives the chosen experts; may be NULL.
  * Reads the router and the three weight matrices of the layer; expert_slot
  * must be NULL (MOE_EUNSUPPORTED otherwise). */
