@@ -717,3 +717,69 @@ def test_adapters_at_the_border_captured(side):
         assert torch.equal(got, y)
         close(got, *adapter_ref(dict(x=x, w=w, base=base, a=a, b=b, scale=None), ids, N))
     M.moe_reader_check_error(ws)
+
+
+# ---------------------------------------------------------- the largest sizes
+def test_block_of_the_most_tokens():
+    """32768 tokens, 16 of 16 experts each: the pairs' fp32 outputs pass 2^31 elements."""
+    E, I, d, top, B = 16, 16, 4096, 16, 32768
+    W = synth.layer_weights(synth.BlockShape(E, I, d, top), seed=60, device="cuda")
+    L = M.Layer(W, top_e=top)
+    x = synth.tokens(d, B, seed=61).cuda()
+    ids = torch.full((B, top), -1, dtype=torch.int32, device="cuda")
+    y = L.forward_grouped(x, ids=ids)
+    L.check()
+    for part in (slice(0, 40), slice(B // 2, B // 2 + 40), slice(B - 40, B)):
+        ref, rid, tol = block_ref(x[part], L.w, top)
+        assert torch.equal(ids[part].long(), rid)
+        close(y[part], ref, tol)
+
+
+@pytest.mark.parametrize("E,I,B,top", [(1024, 16, 3, 16), (1024, 16, 64, 4), (300, 24, 64, 1), (129, 16, 40, 2)])
+def test_block_of_few_tokens_and_many_experts(E, I, B, top):
+    W = synth.layer_weights(synth.BlockShape(E, I, 256, top), seed=62, bias=True, device="cuda")
+    L = M.Layer(W, top_e=top)
+    x = synth.tokens(256, B, seed=63).cuda()
+    ids = torch.full((B, top), -1, dtype=torch.int32, device="cuda")
+    y = L.forward_grouped(x, ids=ids)
+    L.check()
+    ref, rid, tol = block_ref(x, L.w, top)
+    assert torch.equal(ids.long(), rid)
+    close(y, ref, tol)
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_product_outputs_past_32_bits(layout):
+    P, K, N, G = 70000, 16, 32768, 3
+    off = torch.tensor([0, 30000, 30001, P], dtype=torch.int32, device="cuda")
+    rows = torch.randperm(P, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).int()
+    x, w = dev(P, K, seed=64), dev(G, K, N, seed=65) if layout else dev(G, N, K, seed=65)
+    y = torch.empty((P, N), dtype=torch.bfloat16, device="cuda")
+    ws = ws_for(M.moe_reader_grouped_workspace_bytes(G, P))
+    M.moe_reader_grouped_product(G, P, P, P, N, K, layout, x, None, 1, off, w, y, rows, ws, ws.numel())
+    M.moe_reader_check_error(ws)
+    for p in (0, 29999, 30000, 30001, P - 1, int((rows == P - 1).nonzero())):
+        wg = w[0 if p < 30000 else 1 if p == 30000 else 2].double()
+        wg = wg if layout else wg.T
+        ref, mag = x[p].double() @ wg, x[p].double().abs() @ wg.abs()
+        close(y[int(rows[p])], ref, HALF * ref.abs() + SLACK * sum_err(K) * mag)
+
+
+def test_swiglu_outputs_past_32_bits():
+    P, d, I = 140000, 8, 16392
+    off = torch.tensor([0, 70001, P], dtype=torch.int32, device="cuda")
+    x, wg, wu = dev(P, d, seed=66), dev(2, I, d, seed=67), dev(2, I, d, seed=68)
+    a = torch.empty((P, I), dtype=torch.bfloat16, device="cuda")
+    ws = ws_for(M.moe_reader_grouped_workspace_bytes(2, P))
+    M.moe_reader_grouped_swiglu(2, P, P, I, d, x, None, 1, off, wg, wu, a, ws, ws.numel())
+    M.moe_reader_check_error(ws)
+    for part, g in ((slice(0, 3), 0), (slice(70000, 70001), 0), (slice(70001, 70003), 1), (slice(P - 3, P), 1)):
+        ref, e = swiglu_ref(x[part], wg[g], wu[g])
+        close(a[part], ref, HALF * ref.abs() + SLACK * e)
+
+
+def test_adapters_outputs_past_32_bits():
+    T, A, K, N, r = 70000, 3, 16, 32768, 8
+    y, ids, t = adapter_call(T, A, K, N, r, use_base=False)
+    for part in (slice(0, 50), slice(T - 50, T)):
+        close(y[part], *adapter_ref(dict(t, x=t["x"][part]), ids[part], N))
