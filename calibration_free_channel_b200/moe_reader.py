@@ -448,7 +448,8 @@ class Layer:
 
         A captured call gets one that eager calls no longer use and that lives
         as long as the layer: of an earlier capture, or an eager one of before
-        the capture; without any, memory of the graph that each replay zeroes."""
+        the capture; without any, memory of a graph, which every captured call
+        that uses it zeroes first."""
         held = getattr(self, pool)
         if held is None:
             held = {}
@@ -462,6 +463,9 @@ class Layer:
                     del held[h]
                     self._captured.append((pool, True, ws))
                     return ws
+            for p, _, ws in self._captured:
+                if p == pool and ws.numel() >= nb:
+                    return ws.zero_()
             ws = torch.zeros(nb, dtype=torch.uint8, device=self.w["w_gate"].device)
             self._captured.append((pool, False, ws))
             return ws

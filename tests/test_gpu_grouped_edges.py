@@ -783,3 +783,25 @@ def test_adapters_outputs_past_32_bits():
     y, ids, t = adapter_call(T, A, K, N, r, use_base=False)
     for part in (slice(0, 50), slice(T - 50, T)):
         close(y[part], *adapter_ref(dict(t, x=t["x"][part]), ids[part], N))
+
+
+def test_graphs_without_a_call_before_share_their_memory():
+    """Any number of graphs captured without a call before them: one workspace, and each replay is right."""
+    xs = tokens_of(50, 20, 50, 33)
+    L = small_layer()
+    ys = [torch.empty_like(x) for x in xs]
+    graphs = []
+    for x, y in zip(xs, ys):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            L.forward_grouped(x, out=y)
+            L.forward_grouped(x, residual=x, out=y)
+            L.forward_grouped(x, out=y)
+    assert len(L._captured) == 1
+    for g in (graphs[2], graphs[0], graphs[1], graphs[3], graphs[2]):
+        g.replay()
+    torch.cuda.synchronize()
+    other = small_layer()
+    for x, y in zip(xs, ys):
+        assert torch.equal(y, other.forward_grouped(x))
+    L.check()
