@@ -467,6 +467,8 @@ class Layer:
                 if p == pool and ws.numel() >= nb:
                     return ws.zero_()
             ws = torch.zeros(nb, dtype=torch.uint8, device=self.w["w_gate"].device)
+            with torch.cuda.stream(torch.cuda.Stream(ws.device)):
+                ws[:4].zero_()  # at once: check() may come before the first replay
             self._captured.append((pool, False, ws))
             return ws
         ws = held.get(handle)
@@ -610,6 +612,8 @@ class Layer:
         """Raises what the layer's calls recorded on the device since the last
         check; waits for `stream` and for the streams that they ran on."""
         found = None
+        if not all(zeroed for _, zeroed, _ in self._captured):
+            torch.cuda.synchronize(self.w["w_gate"].device)
         held = [(h, ws) for pool in (self._ws, self._wsg) for h, ws in (pool or {}).items()]
         for h, ws in held + [(None, ws) for _, _, ws in self._captured]:
             for s in (stream,) if h is None or h == _stream(stream) else (stream, h):

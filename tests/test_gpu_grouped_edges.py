@@ -805,3 +805,23 @@ def test_graphs_without_a_call_before_share_their_memory():
     for x, y in zip(xs, ys):
         assert torch.equal(y, other.forward_grouped(x))
     L.check()
+
+
+def test_check_before_a_graph_has_run():
+    """A graph's own workspace holds no error before its first replay, whatever its memory held."""
+    x, = tokens_of(50)
+    nb = M.moe_reader_block_workspace_bytes(50, SHAPE.E, 4, SHAPE.I, SHAPE.d)
+    first, g = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(first):
+        junk = torch.full((nb,), 255, dtype=torch.uint8, device="cuda")
+        del junk  # the next graph's workspace gets its memory
+    first.replay()
+    torch.cuda.synchronize()
+    L, y = small_layer(), torch.empty_like(x)
+    with torch.cuda.graph(g, pool=first.pool()):
+        L.forward_grouped(x, out=y)
+    L.check()
+    g.replay()
+    torch.cuda.synchronize()
+    L.check()
+    assert torch.equal(y, L.forward_grouped(x))
