@@ -588,8 +588,8 @@ class Layer:
 
         workspace: of block_workspace, or the layer's own (None), of which it
         keeps one for each stream it is called on.  Pass one to let the layers
-        of a model share it, or where captured graphs of this layer may run at
-        the same time; it has to outlive the graphs, and its errors are read
+        of a model share it, or where captured graphs of this layer (or
+        branches of one) may run at the same time; it has to outlive the graphs, and its errors are read
         by moe_reader_check_error."""
         B = x.shape[0]
         for name, t, shape in (("x", x, (B, self.d)), ("residual", residual, (B, self.d)), ("out", out, (B, self.d)),
